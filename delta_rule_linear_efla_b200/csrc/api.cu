@@ -47,6 +47,7 @@ const char *efla_status_str(int status) {
         case EFLA_ERR_ALIGN: return "pointer not aligned as required";
         case EFLA_ERR_TOO_LARGE: return "sizes exceed the fixed scratch of efla_chunk_fwd_noalloc";
         case EFLA_ERR_RULE: return "unknown update rule";
+        case EFLA_ERR_OPTION: return "unknown option or scalar argument out of range";
         default: return "unknown status";
     }
 }

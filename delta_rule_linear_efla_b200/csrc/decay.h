@@ -1,0 +1,81 @@
+// decay.h -- linear attention with a decay for each head: what its kernels and its entry points
+// share (internal to the library; the public ABI is include/efla.h).
+//
+//   S_t = e^{l_t} S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t.
+//
+// Forward and backward are runs of one "walk" over the tokens, with queries x and keys y of a
+// elements, values z of b elements and a carried state of a x b:
+//
+//   forwards:   out_t = sum_{s <= t} e^{c_t - c_s} (x_t . y_s) z_s + e^{c_t} S^T x_t
+//   backwards:  out_t = sum_{s >= t} e^{c_s - c_t} (x_t . y_s) z_s + e^{c_C - c_t} S^T x_t
+//
+// with c the running sum of l over a stretch of tokens (c_C at its end) and S the state that
+// enters it (from before it, or from behind it).  The state that leaves is e^{c_C} S +
+// sum_s w_s y_s z_s^T with w_s = e^{c_C - c_s} forwards and e^{c_s} backwards.
+//
+//   o  = forwards (q, k, v) from S0           dq = forwards (dO, v, k) from S0^T
+//   dk = backwards (v, dO, q) from dS_final^T  dv = backwards (k, q, dO) from dS_final, ending in dS0
+//   dl_t = sum_{u >= t} (q_u . dq_u - k_u . dk_u) + <dS_final, S_final>
+//
+// The last line: dl_t = e^{l_t} <dL/dS_t, S_{t-1}> = <dL/dS_t, S_t> - k_t . dk_t, and <dL/dS_t, S_t> =
+// q_t . dq_t + dl_{t+1}.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+namespace efla {
+namespace decay {
+
+// The log-decay: [B,H,L] in the input type, or [H] fp32.
+struct Gate {
+    const void *p;
+    int per_head;
+    int bf16;
+    int H;
+};
+
+// One walk.  seg: where the states that enter its segments are kept ([BH][nseg][a][b] fp32; unused
+// with one segment).  dotx / dot: where dot is given, each token's dotx_t . out_t before out is
+// rounded, as shares of the column blocks ([blocks][BH][L] fp32, added by the gradient kernel).
+struct Walk {
+    const void *x, *y, *z;
+    const float *s0;  // the state that enters, or null for zero
+    int s0_t;         // s0 is stored transposed ([b][a])
+    void *out;
+    float *s_end;     // the state that leaves, or null
+    int a, b, rev;
+    const void *dotx;
+    float *dot;
+    float *seg;
+};
+
+constexpr int MAX_WALKS = 3;
+struct Walks {
+    Walk w[MAX_WALKS];
+    int n;
+};
+
+constexpr int C = 64;             // tokens in a chunk
+constexpr float L_MIN = -200.f;   // e^L_MIN is 0 in fp32: lower log-decays (-inf) act as this one
+
+// CUDA-core walks: any a, b <= 128, fp32 arithmetic; blocks of SIMT_BT value columns.
+constexpr int SIMT_BT = 32;
+int simt_segments(int BH, int L, const int *blocks, int n);
+cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool in_bf16,
+                              bool out_bf16, cudaStream_t s);
+
+// States of the segments: from every segment's own contribution (in seg, in walking order) and its
+// whole decay e^{sum l} (seg_e [BH][nseg]) to the state that enters it.
+cudaError_t launch_seg_chain(const Walks &ws, const float *seg_e, int BH, int nseg, cudaStream_t s);
+
+// dl from the walks' dots: dotq [nq][BH][L], dotk [nk][BH][L] (shares of their column blocks);
+// dS_final [BH][dk][dv] and the forward walk's end state S_end [BH][dv][dk], or both null.
+cudaError_t launch_dlog(const float *dotq, int nq, const float *dotk, int nk, const float *dS_final,
+                        const float *S_end, Gate g, void *dlog, int BH, int L, int dk, int dv, cudaStream_t s);
+
+cudaError_t launch_step(const void *q, const void *k, const void *v, Gate g, float *S, void *o, int BH, int dk,
+                        int dv, bool in_bf16, bool o_bf16, cudaStream_t s);
+
+}  // namespace decay
+}  // namespace efla

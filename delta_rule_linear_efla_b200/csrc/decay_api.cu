@@ -1,0 +1,203 @@
+// decay_api.cu -- extern "C" entry points of linear attention with a decay for each head
+// (include/efla.h): argument checks, workspace layout and the choice of kernels.
+#include <stdint.h>
+
+#include "../../include/efla.h"
+#include "decay.h"
+#include "launchers.h"
+
+namespace {
+
+using efla::decay::Gate;
+using efla::decay::Walk;
+using efla::decay::Walks;
+
+bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+size_t elem(efla_dtype dt) { return dt == EFLA_BF16 ? 2 : 4; }
+bool dtype_ok(efla_dtype d) { return d == EFLA_F32 || d == EFLA_BF16; }
+bool form_ok(efla_decay_form f) { return f == EFLA_DECAY_TOKEN || f == EFLA_DECAY_HEAD; }
+efla_status from_cuda(cudaError_t e) { return e == cudaSuccess ? EFLA_OK : EFLA_ERR_CUDA; }
+size_t gate_elem(efla_decay_form f, efla_dtype dt) { return f == EFLA_DECAY_HEAD ? 4 : elem(dt); }
+
+constexpr long long MAX_HEADS = 1 << 24;  // B * H: grids stay below 2^31 blocks
+
+bool sizes_ok(int B, int H, long long L, int dk, int dv) {
+    return B >= 1 && H >= 1 && L >= 0 && dk >= 1 && dv >= 1 && (long long)B * H <= MAX_HEADS && L <= 0x7fffff00LL &&
+           (long long)B * H * L <= (1LL << 40);
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+// A bump allocator over the caller's workspace; with a null base it only counts.
+struct Arena {
+    char *base;
+    size_t used = 0;
+    float *floats(size_t n) {
+        float *p = base ? reinterpret_cast<float *>(base + used) : nullptr;
+        used += up(n * sizeof(float));
+        return p;
+    }
+};
+
+int blocks_of(int b) { return (b + efla::decay::SIMT_BT - 1) / efla::decay::SIMT_BT; }
+
+// The walks' segments and their states: lays them out in the arena.
+int plan_segments(Walks &ws, int BH, int L, Arena &ar, float **seg_e) {
+    int blocks[efla::decay::MAX_WALKS];
+    for (int i = 0; i < ws.n; ++i) blocks[i] = blocks_of(ws.w[i].b);
+    const int nseg = efla::decay::simt_segments(BH, L, blocks, ws.n);
+    *seg_e = nullptr;
+    if (nseg > 1) {
+        for (int i = 0; i < ws.n; ++i) ws.w[i].seg = ar.floats((size_t)BH * nseg * ws.w[i].a * ws.w[i].b);
+        *seg_e = ar.floats((size_t)2 * BH * nseg);
+    }
+    return nseg;
+}
+
+struct FwdPlan {
+    Walks ws{};
+    float *seg_e = nullptr;
+    int nseg = 1;
+    size_t bytes = 0;
+    FwdPlan(int BH, int L, int dk, int dv, void *base) {
+        Arena ar{static_cast<char *>(base)};
+        ws.n = 1;
+        ws.w[0].a = dk;
+        ws.w[0].b = dv;
+        nseg = plan_segments(ws, BH, L, ar, &seg_e);
+        bytes = ar.used;
+    }
+};
+
+struct BwdPlan {
+    Walks ws{};  // dq, dk, dv
+    float *seg_e = nullptr, *S_end = nullptr, *dotq = nullptr, *dotk = nullptr;
+    int nseg = 1, nq = 1, nk = 1;
+    size_t bytes = 0;
+    BwdPlan(int BH, int L, int dk, int dv, void *base) {
+        Arena ar{static_cast<char *>(base)};
+        ws.n = 3;
+        ws.w[0].a = dv; ws.w[0].b = dk;
+        ws.w[1].a = dv; ws.w[1].b = dk; ws.w[1].rev = 1;
+        ws.w[2].a = dk; ws.w[2].b = dv; ws.w[2].rev = 1;
+        nq = nk = blocks_of(dk);
+        dotq = ar.floats((size_t)nq * BH * L);
+        dotk = ar.floats((size_t)nk * BH * L);
+        S_end = ar.floats((size_t)BH * dk * dv);
+        nseg = plan_segments(ws, BH, L, ar, &seg_e);
+        bytes = ar.used;
+    }
+};
+
+}  // namespace
+
+extern "C" {
+
+size_t efla_decay_chunk_fwd_workspace_size(int B, int H, int L, int dk, int dv, efla_dtype dt) {
+    if (!dtype_ok(dt) || !sizes_ok(B, H, L, dk, dv) || L == 0 || dk > 128 || dv > 128) return 0;
+    return FwdPlan(B * H, L, dk, dv, nullptr).bytes;
+}
+
+efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, const void *log_g,
+                                 efla_decay_form form, const float *S0, void *o, float *S_final, int B, int H, int L,
+                                 int dk, int dv, efla_dtype dt, efla_dtype o_dt, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+    if (!dtype_ok(dt) || !dtype_ok(o_dt)) return EFLA_ERR_DTYPE;
+    if (!form_ok(form)) return EFLA_ERR_OPTION;
+    if (!sizes_ok(B, H, L, dk, dv)) return EFLA_ERR_SHAPE;
+    if (dk > 128 || dv > 128) return EFLA_ERR_UNSUPPORTED;
+    if (L > 0 && (!q || !k || !v || !log_g || !o)) return EFLA_ERR_NULL;
+    if (!aligned(q, elem(dt)) || !aligned(k, elem(dt)) || !aligned(v, elem(dt)) || !aligned(o, elem(o_dt)) ||
+        !aligned(log_g, gate_elem(form, dt)) || !aligned(S0, 4) || !aligned(S_final, 4) || !aligned(workspace, 16))
+        return EFLA_ERR_ALIGN;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int BH = B * H;
+    const size_t state = (size_t)BH * dk * dv * sizeof(float);
+    if (L == 0) {
+        if (!S_final || S0 == S_final) return EFLA_OK;
+        return from_cuda(S0 ? cudaMemcpyAsync(S_final, S0, state, cudaMemcpyDeviceToDevice, s)
+                            : cudaMemsetAsync(S_final, 0, state, s));
+    }
+    FwdPlan p(BH, L, dk, dv, workspace);
+    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return EFLA_ERR_WORKSPACE;
+    Walk &w = p.ws.w[0];
+    w.x = q; w.y = k; w.z = v;
+    w.s0 = S0;
+    w.out = o;
+    w.s_end = S_final;
+    const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
+    return from_cuda(efla::decay::launch_walks_simt(p.ws, g, BH, L, p.nseg, p.seg_e, dt == EFLA_BF16,
+                                                    o_dt == EFLA_BF16, s));
+}
+
+size_t efla_decay_bwd_workspace_size(int B, int H, int L, int dk, int dv, efla_dtype dt) {
+    if (!dtype_ok(dt) || !sizes_ok(B, H, L, dk, dv) || L == 0 || dk > 128 || dv > 128) return 0;
+    return BwdPlan(B * H, L, dk, dv, nullptr).bytes;
+}
+
+efla_status efla_decay_bwd(const void *q, const void *k, const void *v, const void *log_g, efla_decay_form form,
+                           const float *S0, const void *dO, const float *dS_final, void *dq, void *dkey, void *dval,
+                           void *dlog_g, float *dS0, int B, int H, int L, int dk, int dv, efla_dtype dt,
+                           void *workspace, size_t workspace_bytes, void *stream) {
+    if (!dtype_ok(dt)) return EFLA_ERR_DTYPE;
+    if (!form_ok(form) || (form == EFLA_DECAY_HEAD && dlog_g)) return EFLA_ERR_OPTION;
+    if (!sizes_ok(B, H, L, dk, dv)) return EFLA_ERR_SHAPE;
+    if (dk > 128 || dv > 128) return EFLA_ERR_UNSUPPORTED;
+    if (L > 0 && (!q || !k || !v || !log_g || !dO || !dq || !dkey || !dval)) return EFLA_ERR_NULL;
+    const void *in[] = {q, k, v, dO, dq, dkey, dval, dlog_g};
+    for (const void *p : in)
+        if (!aligned(p, elem(dt))) return EFLA_ERR_ALIGN;
+    if (!aligned(log_g, gate_elem(form, dt)) || !aligned(S0, 4) || !aligned(dS_final, 4) || !aligned(dS0, 4) ||
+        !aligned(workspace, 16))
+        return EFLA_ERR_ALIGN;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int BH = B * H;
+    const size_t state = (size_t)BH * dk * dv * sizeof(float);
+    if (L == 0) {
+        if (!dS0) return EFLA_OK;
+        return from_cuda(dS_final ? cudaMemcpyAsync(dS0, dS_final, state, cudaMemcpyDeviceToDevice, s)
+                                  : cudaMemsetAsync(dS0, 0, state, s));
+    }
+    BwdPlan p(BH, L, dk, dv, workspace);
+    if (!workspace || workspace_bytes < p.bytes) return EFLA_ERR_WORKSPACE;
+    const bool want_dl = dlog_g != nullptr, tail = want_dl && dS_final;
+    Walk &a = p.ws.w[0], &b = p.ws.w[1], &c = p.ws.w[2];
+    a.x = dO; a.y = v; a.z = k;
+    a.s0 = S0; a.s0_t = 1;
+    a.out = dq;
+    a.s_end = tail ? p.S_end : nullptr;
+    b.x = v; b.y = dO; b.z = q;
+    b.s0 = dS_final; b.s0_t = 1;
+    b.out = dkey;
+    c.x = k; c.y = q; c.z = dO;
+    c.s0 = dS_final;
+    c.out = dval;
+    c.s_end = dS0;
+    if (want_dl) {
+        a.dotx = q; a.dot = p.dotq;
+        b.dotx = k; b.dot = p.dotk;
+    }
+    const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
+    cudaError_t e = efla::decay::launch_walks_simt(p.ws, g, BH, L, p.nseg, p.seg_e, dt == EFLA_BF16, dt == EFLA_BF16, s);
+    if (e != cudaSuccess || !want_dl) return from_cuda(e);
+    return from_cuda(efla::decay::launch_dlog(p.dotq, p.nq, p.dotk, p.nk, dS_final, tail ? p.S_end : nullptr, g, dlog_g,
+                                              BH, L, dk, dv, s));
+}
+
+efla_status efla_decay_recurrent_step(const void *q, const void *k, const void *v, const void *log_g,
+                                      efla_decay_form form, float *S, void *o, int B, int H, int dk, int dv,
+                                      efla_dtype dt, efla_dtype o_dt, void *stream) {
+    if (!dtype_ok(dt) || !dtype_ok(o_dt)) return EFLA_ERR_DTYPE;
+    if (!form_ok(form)) return EFLA_ERR_OPTION;
+    if (!sizes_ok(B, H, 1, dk, dv)) return EFLA_ERR_SHAPE;
+    if (dk > 256 || dv > 256) return EFLA_ERR_UNSUPPORTED;
+    if (!q || !k || !v || !log_g || !S || !o) return EFLA_ERR_NULL;
+    if (!aligned(q, elem(dt)) || !aligned(k, elem(dt)) || !aligned(v, elem(dt)) || !aligned(o, elem(o_dt)) ||
+        !aligned(log_g, gate_elem(form, dt)) || !aligned(S, 16))
+        return EFLA_ERR_ALIGN;
+    const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
+    return from_cuda(efla::decay::launch_step(q, k, v, g, S, o, B * H, dk, dv, dt == EFLA_BF16, o_dt == EFLA_BF16,
+                                              (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,433 @@
+// decay_simt.cu -- linear attention with a decay for each head on CUDA cores: fp32 inputs, and
+// head sizes that the tensor-core walks do not take.
+//
+// One CTA walks one stretch of one head for SIMT_BT = 32 value columns (columns of the state do not
+// depend on one another), a chunk of 64 tokens at a time, everything in fp32:
+//
+//   P = D o (X Y^T) (64 x 64),   out = diag(q) X S + P Z,   S <- e^{c_C} S + Y^T diag(w) Z
+//
+// with D, q and w the decay weights of decay.h.  Every product is register-tiled out of shared
+// memory (4 x 4 or 4 x 2 outputs a thread, 16-byte loads along the inner dimension), so the FMA pipe
+// and shared memory take about the same time.  32 columns keep a CTA at 113 KB, two to an SM, so
+// that one's loads run under the other's arithmetic; P is computed again in each column block.
+#include "decay_gate.cuh"
+#include "launchers.h"
+
+namespace efla {
+namespace decay {
+
+namespace {
+
+constexpr int NT = 256;
+constexpr int BT = SIMT_BT;
+constexpr int ZP = BT + 4, PP = C + 4;
+
+struct Lay {
+    int ap, xp;  // a rounded up to 4, and the row stride of X and Y
+    int oX, oY, oZ, oP, oS, oG, total;
+    __host__ __device__ explicit Lay(int a) {
+        ap = (a + 3) & ~3;
+        xp = ap + 4;
+        oX = 0;
+        oY = oX + C * xp;
+        oZ = oY + C * xp;
+        oP = oZ + C * ZP;
+        oS = oP + C * PP;
+        oG = oS + ap * ZP;
+        total = (oG + 4 * C + 4) * (int)sizeof(float);
+    }
+};
+
+// rows [t0, t0 + C) of a [L][d] tensor, columns [j0, j0 + n), zero past L and past d.
+template <typename T>
+__device__ __forceinline__ void load_tile(float *dst, int pitch, const T *src, int d, int j0, int n, int cl,
+                                          int tid) {
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = (reinterpret_cast<uintptr_t>(src) % 16 == 0) && d % V == 0 && n % V == 0 && j0 + n <= d;
+    if (vec) {
+        const int per = n / V;
+        for (int e = tid; e < C * per; e += NT) {
+            const int r = e / per, c = (e - r * per) * V;
+            float f[V];
+            if (r < cl) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(src + (size_t)r * d + j0 + c);
+                const T *h = reinterpret_cast<const T *>(&u);
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] = to_f32(h[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4 *>(dst + r * pitch + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+        }
+    } else {
+        for (int e = tid; e < C * n; e += NT) {
+            const int r = e / n, c = e - r * n;
+            dst[r * pitch + c] = (r < cl && j0 + c < d) ? to_f32(src[(size_t)r * d + j0 + c]) : 0.f;
+        }
+    }
+}
+
+__device__ __forceinline__ void fma4(float (&acc)[4], float s, const float4 &v) {
+    acc[0] = fmaf(s, v.x, acc[0]);
+    acc[1] = fmaf(s, v.y, acc[1]);
+    acc[2] = fmaf(s, v.z, acc[2]);
+    acc[3] = fmaf(s, v.w, acc[3]);
+}
+
+// OUT = false: the stretch's own contribution to the state only (segments' first pass).
+template <typename T, typename TO, bool OUT>
+__global__ void __launch_bounds__(NT, 2)
+    walk_simt_kernel(const __grid_constant__ Walks ws, const Gate g, int BH, int L, int nseg, int seg_chunks,
+                     float *__restrict__ seg_e) {
+    extern __shared__ __align__(16) float sm[];
+    // ---- which walk, column block and head: blockIdx.x = (block of all walks) * BH + bh
+    const int bh = blockIdx.x % BH;
+    int blk = blockIdx.x / BH, wi = 0;
+    while (wi + 1 < ws.n && blk >= (ws.w[wi].b + BT - 1) / BT) {
+        blk -= (ws.w[wi].b + BT - 1) / BT;
+        ++wi;
+    }
+    const Walk &w = ws.w[wi];
+    const int a = w.a, b = w.b, j0 = blk * BT, nb = min(BT, b - j0);
+    const bool rev = w.rev != 0;
+    const Lay lay(a);
+    float *X = sm + lay.oX, *Y = sm + lay.oY, *Z = sm + lay.oZ, *P = sm + lay.oP, *S = sm + lay.oS;
+    float *qw = sm + lay.oG, *kw = qw + C, *chi = kw + C, *clo = chi + C, *tot = clo + C;
+    const int xp = lay.xp, ap = lay.ap;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int NC = (L + C - 1) / C;
+    const int seg = blockIdx.y;  // in walking order
+    const int i0 = seg * seg_chunks, i1 = min(NC, i0 + seg_chunks);
+
+    // ---- the state that enters
+    const size_t sbh = (size_t)bh * a * b;
+    const float *sin = nullptr;
+    if (OUT) sin = nseg > 1 ? w.seg + ((size_t)bh * nseg + seg) * a * b : (w.s0 ? w.s0 + sbh : nullptr);
+    const bool st = nseg == 1 && w.s0_t;
+    for (int e = tid; e < ap * BT; e += NT) {
+        const int i = e / BT, j = e % BT;
+        float v = 0.f;
+        if (sin && i < a && j < nb) v = st ? sin[(size_t)(j0 + j) * a + i] : sin[(size_t)i * b + j0 + j];
+        S[i * ZP + j] = v;
+    }
+    double seg_sum = 0.0;
+
+    const int r4 = (tid >> 4) * 4, tc = tid & 15;  // P: rows r4.., columns tc + 16 j; out: columns 2 tc, 2 tc + 1
+    for (int it = i0; it < i1; ++it) {
+        const int n = rev ? NC - 1 - it : it;
+        const int t0 = n * C, cl = min(C, L - t0);
+        const size_t row0 = (size_t)bh * L + t0;
+        __syncthreads();  // the chunk before is done with every buffer
+        if (OUT) load_tile(X, xp, static_cast<const T *>(w.x) + row0 * a, a, 0, ap, cl, tid);
+        load_tile(Y, xp, static_cast<const T *>(w.y) + row0 * a, a, 0, ap, cl, tid);
+        load_tile(Z, ZP, static_cast<const T *>(w.z) + row0 * b, b, j0, BT, cl, tid);
+        if (warp == 0) {
+            const PairSum c = chunk_sums(g, bh, L, t0, lane);
+            const double cC = __shfl_sync(0xffffffffu, c.c1, 31);
+            const double cc[2] = {c.c0, c.c1};
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                const float up = exp_sum(cc[e]), down = exp_sum(cC - cc[e]);
+                qw[t] = rev ? down : up;
+                kw[t] = rev ? up : down;
+                chi[t] = (float)cc[e];
+                clo[t] = (float)(cc[e] - (double)(float)cc[e]);
+            }
+            if (lane == 0) tot[0] = exp_sum(cC);
+            seg_sum += cC;
+        }
+        __syncthreads();
+        if (OUT) {
+            // ---- P = D o (X Y^T): 4 x 4 a thread
+            float p[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[i][j] = 0.f;
+            for (int k = 0; k < ap; k += 4) {
+                float4 xv[4], yv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const float4 *>(X + (r4 + i) * xp + k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) yv[j] = *reinterpret_cast<const float4 *>(Y + (tc + 16 * j) * xp + k);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        p[i][j] = fmaf(xv[i].x, yv[j].x, fmaf(xv[i].y, yv[j].y, fmaf(xv[i].z, yv[j].z, fmaf(xv[i].w, yv[j].w, p[i][j]))));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = r4 + i, c = tc + 16 * j;
+                    const float d = (chi[r] - chi[c]) + (clo[r] - clo[c]);
+                    const bool on = rev ? c >= r : c <= r;
+                    P[r * PP + c] = on ? p[i][j] * expf(rev ? -d : d) : 0.f;
+                }
+            __syncthreads();
+            // ---- out = diag(q) X S + P Z: 4 rows x 2 columns a thread
+            float o[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i][0] = o[i][1] = 0.f;
+            const int cc = 2 * tc;
+            for (int k = 0; k < ap; k += 4) {
+                float4 xv[4];
+                float2 sv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const float4 *>(X + (r4 + i) * xp + k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sv[j] = *reinterpret_cast<const float2 *>(S + (k + j) * ZP + cc);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[i][0] = fmaf(xv[i].x, sv[0].x, fmaf(xv[i].y, sv[1].x, fmaf(xv[i].z, sv[2].x, fmaf(xv[i].w, sv[3].x, o[i][0]))));
+                    o[i][1] = fmaf(xv[i].x, sv[0].y, fmaf(xv[i].y, sv[1].y, fmaf(xv[i].z, sv[2].y, fmaf(xv[i].w, sv[3].y, o[i][1]))));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[i][0] *= qw[r4 + i];
+                o[i][1] *= qw[r4 + i];
+            }
+            const int k0 = rev ? r4 : 0, k1 = rev ? C : r4 + 4;  // the rest of P's rows is zero
+            for (int k = k0; k < k1; k += 4) {
+                float4 pv[4];
+                float2 zv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) pv[i] = *reinterpret_cast<const float4 *>(P + (r4 + i) * PP + k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) zv[j] = *reinterpret_cast<const float2 *>(Z + (k + j) * ZP + cc);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[i][0] = fmaf(pv[i].x, zv[0].x, fmaf(pv[i].y, zv[1].x, fmaf(pv[i].z, zv[2].x, fmaf(pv[i].w, zv[3].x, o[i][0]))));
+                    o[i][1] = fmaf(pv[i].x, zv[0].y, fmaf(pv[i].y, zv[1].y, fmaf(pv[i].z, zv[2].y, fmaf(pv[i].w, zv[3].y, o[i][1]))));
+                }
+            }
+            TO *out = static_cast<TO *>(w.out) + row0 * b + j0;
+            const T *dx = w.dot ? static_cast<const T *>(w.dotx) + row0 * b + j0 : nullptr;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = r4 + i;
+                float dd = 0.f;
+                if (r < cl) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (cc + j < nb) {
+                            out[(size_t)r * b + cc + j] = from_f32<TO>(o[i][j]);
+                            if (dx) dd = fmaf(to_f32(dx[(size_t)r * b + cc + j]), o[i][j], dd);
+                        }
+                }
+                if (dx) {  // the row's 16 threads are half a warp
+#pragma unroll
+                    for (int off = 8; off > 0; off >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
+                    if (tc == 0 && r < cl) w.dot[((size_t)blk * BH + bh) * L + t0 + r] = dd;
+                }
+            }
+            __syncthreads();  // the state is read
+        }
+        // ---- S <- e^{c_C} S + Y^T diag(w) Z: 4 x 4 a thread
+        const float e = tot[0];
+        const int sc = (tid & 7) * 4;
+        for (int si = (tid >> 3) * 4; si < ap; si += (NT / 8) * 4) {
+            float acc[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+            for (int t = 0; t < C; ++t) {
+                const float4 yv = *reinterpret_cast<const float4 *>(Y + t * xp + si);
+                float4 zv = *reinterpret_cast<const float4 *>(Z + t * ZP + sc);
+                const float f = kw[t];
+                zv.x *= f; zv.y *= f; zv.z *= f; zv.w *= f;
+                fma4(acc[0], yv.x, zv);
+                fma4(acc[1], yv.y, zv);
+                fma4(acc[2], yv.z, zv);
+                fma4(acc[3], yv.w, zv);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float4 *s4 = reinterpret_cast<float4 *>(S + (si + i) * ZP + sc);
+                float4 s = *s4;
+                s.x = fmaf(e, s.x, acc[i][0]); s.y = fmaf(e, s.y, acc[i][1]);
+                s.z = fmaf(e, s.z, acc[i][2]); s.w = fmaf(e, s.w, acc[i][3]);
+                *s4 = s;
+            }
+        }
+    }
+    __syncthreads();
+    float *sout = nullptr;
+    if (!OUT) sout = w.seg + ((size_t)bh * nseg + seg) * a * b;
+    else if (seg == nseg - 1 && w.s_end) sout = w.s_end + sbh;
+    if (sout) {
+        for (int e = tid; e < a * BT; e += NT) {
+            const int i = e / BT, j = e % BT;
+            if (j < nb) sout[(size_t)i * b + j0 + j] = S[i * ZP + j];
+        }
+    }
+    // every walk in the same direction finds the same decay of a segment: its first one writes it
+    if (!OUT && warp == 0 && lane == 0 && blk == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
+        seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp_sum(seg_sum);
+}
+
+template <typename T, typename TO>
+cudaError_t launch_t(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, cudaStream_t s) {
+    int blocks = 0, smem = 0;
+    for (int i = 0; i < ws.n; ++i) {
+        blocks += (ws.w[i].b + BT - 1) / BT;
+        const int t = Lay(ws.w[i].a).total;
+        smem = t > smem ? t : smem;
+    }
+    const int NC = (L + C - 1) / C, per = (NC + nseg - 1) / nseg;
+    auto *full = walk_simt_kernel<T, TO, true>;
+    auto *part = walk_simt_kernel<T, TO, false>;
+    cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && nseg > 1) e = cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (nseg > 1) {
+        part<<<dim3(blocks * BH, nseg - 1), NT, smem, s>>>(ws, g, BH, L, nseg, per, seg_e);
+        count_launches(1);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch_seg_chain(ws, seg_e, BH, nseg, s);
+        if (e != cudaSuccess) return e;
+    }
+    full<<<dim3(blocks * BH, nseg), NT, smem, s>>>(ws, g, BH, L, nseg, per, seg_e);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+// One thread per state element: S_0 is the state that enters the walk, S_{i+1} = e_i S_i + U_i; U_i is
+// read from where S_i is written.
+__global__ void __launch_bounds__(256)
+    seg_chain_kernel(const __grid_constant__ Walks ws, const float *__restrict__ seg_e, int BH, int nseg) {
+    const Walk &w = ws.w[blockIdx.z];
+    const int ab = w.a * w.b, bh = blockIdx.x;
+    const float *ee = seg_e + ((size_t)(w.rev ? 1 : 0) * BH + bh) * nseg;
+    for (int e = blockIdx.y * 256 + threadIdx.x; e < ab; e += gridDim.y * 256) {
+        const int i = e / w.b, j = e - i * w.b;
+        float s = w.s0 ? w.s0[(size_t)bh * ab + (w.s0_t ? j * w.a + i : e)] : 0.f;
+        float *p = w.seg + (size_t)bh * nseg * ab + e;
+        for (int k = 0; k < nseg; ++k) {
+            const float u = k + 1 < nseg ? p[(size_t)k * ab] : 0.f;
+            p[(size_t)k * ab] = s;
+            if (k + 1 < nseg) s = fmaf(ee[k], s, u);
+        }
+    }
+}
+
+constexpr int DL_T = 512, DL_E = 8;
+
+// One CTA per head, tokens from the end: a block-wide suffix sum in fp64 (the differences q.dq - k.dk
+// of a long sequence cancel down to the pairs that straddle a token).
+template <typename T>
+__global__ void __launch_bounds__(DL_T)
+    dlog_kernel(const float *__restrict__ dotq, int nq, const float *__restrict__ dotk, int nk,
+                const float *__restrict__ dS, const float *__restrict__ S_end, const Gate g, T *__restrict__ dlog,
+                int BH, int L, int dk, int dv) {
+    __shared__ double part[DL_T / 32];
+    __shared__ double carry_s;
+    const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    double carry = 0.0;
+    if (dS) {  // <dS_final, S_final>
+        const size_t base = (size_t)bh * dk * dv;
+        double t = 0.0;
+        for (int e = tid; e < dk * dv; e += DL_T) {
+            const int i = e / dk, j = e - i * dk;  // S_end is [dv][dk]
+            t += (double)S_end[base + e] * (double)dS[base + (size_t)j * dv + i];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+        if (lane == 0) part[warp] = t;
+        __syncthreads();
+        for (int i = 0; i < DL_T / 32; ++i) carry += part[i];
+        __syncthreads();
+    }
+    const size_t row = (size_t)bh * L, plane = (size_t)BH * L;
+    for (int hi = L; hi > 0; hi -= DL_T * DL_E) {
+        // thread tid holds tokens hi - 1 - (tid DL_E + e), e = 0 .. DL_E - 1
+        double x[DL_E], sum = 0.0;
+#pragma unroll
+        for (int e = 0; e < DL_E; ++e) {
+            const int t = hi - 1 - (tid * DL_E + e);
+            double v = 0.0;
+            if (t >= 0) {
+                for (int i = 0; i < nq; ++i) v += (double)dotq[i * plane + row + t];
+                for (int i = 0; i < nk; ++i) v -= (double)dotk[i * plane + row + t];
+            }
+            sum += v;
+            x[e] = sum;
+        }
+        double s = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        if (lane == 31) part[warp] = s;
+        __syncthreads();
+        double before = carry;
+        for (int i = 0; i < warp; ++i) before += part[i];
+        const double off = before + (s - sum);
+#pragma unroll
+        for (int e = 0; e < DL_E; ++e) {
+            const int t = hi - 1 - (tid * DL_E + e);
+            if (t >= 0) {
+                // a token that forgets everything: d e^l / dl = 0
+                const bool forgets = gate_at(g, bh, L, t) == L_MIN;
+                dlog[row + t] = from_f32<T>(forgets ? 0.f : (float)(off + x[e]));
+            }
+        }
+        if (tid == DL_T - 1) carry_s = off + sum;
+        __syncthreads();
+        carry = carry_s;
+    }
+}
+
+}  // namespace
+
+int simt_segments(int BH, int L, const int *blocks, int n) {
+    // A segment run more costs about a third of a walk (the state update alone); below about one CTA
+    // an SM the sequence is cut until the device is full, at four chunks a segment or more.
+    long long ctas = 0;
+    for (int i = 0; i < n; ++i) ctas += (long long)blocks[i] * BH;
+    const int NC = (L + C - 1) / C;
+    if (ctas >= 148 || NC < 8) return 1;
+    long long want = (2 * 148 + ctas - 1) / ctas;
+    if (want > NC / 4) want = NC / 4;
+    if (want < 2) return 1;
+    const int per = (int)((NC + want - 1) / want);
+    return (NC + per - 1) / per;
+}
+
+cudaError_t launch_seg_chain(const Walks &ws, const float *seg_e, int BH, int nseg, cudaStream_t s) {
+    int ab = 1;
+    for (int i = 0; i < ws.n; ++i) ab = ws.w[i].a * ws.w[i].b > ab ? ws.w[i].a * ws.w[i].b : ab;
+    seg_chain_kernel<<<dim3(BH, (ab + 255) / 256, ws.n), 256, 0, s>>>(ws, seg_e, BH, nseg);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool in_bf16,
+                              bool out_bf16, cudaStream_t s) {
+    using bf = __nv_bfloat16;
+    if (in_bf16)
+        return out_bf16 ? launch_t<bf, bf>(ws, g, BH, L, nseg, seg_e, s) : launch_t<bf, float>(ws, g, BH, L, nseg, seg_e, s);
+    return out_bf16 ? launch_t<float, bf>(ws, g, BH, L, nseg, seg_e, s) : launch_t<float, float>(ws, g, BH, L, nseg, seg_e, s);
+}
+
+cudaError_t launch_dlog(const float *dotq, int nq, const float *dotk, int nk, const float *dS_final,
+                        const float *S_end, Gate g, void *dlog, int BH, int L, int dk, int dv, cudaStream_t s) {
+    if (g.bf16)
+        dlog_kernel<__nv_bfloat16><<<BH, DL_T, 0, s>>>(dotq, nq, dotk, nk, dS_final, S_end, g, (__nv_bfloat16 *)dlog, BH, L, dk, dv);
+    else
+        dlog_kernel<float><<<BH, DL_T, 0, s>>>(dotq, nq, dotk, nk, dS_final, S_end, g, (float *)dlog, BH, L, dk, dv);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+}  // namespace decay
+}  // namespace efla

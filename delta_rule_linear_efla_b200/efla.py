@@ -28,6 +28,9 @@ ABI_SYMBOLS = (
     "efla_recurrent_step_rule", "efla_state_affine", "efla_bwd_workspace_size", "efla_bwd",
     "efla_selftest_bounded_wait", "efla_chunk_fwd_gated", "efla_recurrent_step_gated",
     "efla_bwd_kept_size", "efla_chunk_fwd_keep", "efla_bwd_kept",
+    "efla_decay_chunk_fwd_workspace_size", "efla_decay_chunk_fwd", "efla_decay_bwd_workspace_size",
+    "efla_decay_bwd", "efla_decay_recurrent_step", "efla_norm_bwd_workspace_size", "efla_head_norm",
+    "efla_head_norm_bwd", "efla_gated_norm", "efla_gated_norm_bwd",
 )
 
 _lib = None
@@ -94,6 +97,27 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     L.efla_bwd_kept.argtypes = [vp] * 12 + [i] * 7 + [vp, sz, vp, sz, vp]
     L.efla_bwd_kept_size.restype = sz
     L.efla_bwd_kept_size.argtypes = [i, i, i, i, i]
+    f = ctypes.c_float
+    L.efla_decay_chunk_fwd_workspace_size.restype = sz
+    L.efla_decay_chunk_fwd_workspace_size.argtypes = [i] * 6
+    L.efla_decay_chunk_fwd.restype = i
+    L.efla_decay_chunk_fwd.argtypes = [vp] * 4 + [i] + [vp] * 3 + [i] * 7 + [vp, sz, vp]
+    L.efla_decay_bwd_workspace_size.restype = sz
+    L.efla_decay_bwd_workspace_size.argtypes = [i] * 6
+    L.efla_decay_bwd.restype = i
+    L.efla_decay_bwd.argtypes = [vp] * 4 + [i] + [vp] * 8 + [i] * 6 + [vp, sz, vp]
+    L.efla_decay_recurrent_step.restype = i
+    L.efla_decay_recurrent_step.argtypes = [vp] * 4 + [i] + [vp] * 2 + [i] * 6 + [vp]
+    L.efla_norm_bwd_workspace_size.restype = sz
+    L.efla_norm_bwd_workspace_size.argtypes = [i]
+    L.efla_head_norm.restype = i
+    L.efla_head_norm.argtypes = [vp, vp, vp, i, vp] + [i] * 6 + [f, f, vp]
+    L.efla_head_norm_bwd.restype = i
+    L.efla_head_norm_bwd.argtypes = [vp, vp, vp, i, vp, vp, vp] + [i] * 6 + [f, f, vp, sz, vp]
+    L.efla_gated_norm.restype = i
+    L.efla_gated_norm.argtypes = [vp, i, vp, vp, vp, i, vp, vp, vp] + [i] * 6 + [f, f, vp]
+    L.efla_gated_norm_bwd.restype = i
+    L.efla_gated_norm_bwd.argtypes = [vp, i, vp, vp, vp, i] + [vp] * 4 + [i] * 6 + [f, f, vp, sz, vp]
     if path is None:
         _lib = L
     return L
@@ -385,9 +409,18 @@ class EflaFunction(torch.autograd.Function):
                 dS0 if ctx.has_S0 else None, None, None)
 
 
-def efla_attention(q, k, v, beta, S0=None, rule: str = "exact", chunk: int = 64):
-    """Differentiable EFLA forward: (o, S_final) with gradients through efla_bwd."""
-    return EflaFunction.apply(q, k, v, beta, S0, rule, chunk)
+def efla_attention(q, k, v, beta, S0=None, rule: str = "exact", chunk: int = 64, *, qk_norm: str | None = None,
+                   gate=None, norm_weight=None, residual=None, scale: float = 1.0, eps: float = 1e-6,
+                   act: str = "silu"):
+    """Differentiable EFLA forward: (o, S_final) with gradients through efla_bwd.
+
+    qk_norm ("l2" or "rms") normalises q and k per head before it (norms.head_norm).  With a gate
+    ([B,L,H,dv]) the output goes through norms.gated_norm, with norm_weight ([dv]), residual
+    ([B,L,H,dv]), scale and act, and is [B,L,H,dv] in the gate's dtype."""
+    from .norms import normed_attention
+
+    return normed_attention(lambda q, k: EflaFunction.apply(q, k, v, beta, S0, rule, chunk), q, k, qk_norm, gate,
+                            norm_weight, residual, scale, eps, act)
 
 
 def selftest_bounded_wait(budget_cycles: int = 1_000_000, stream=None) -> None:

@@ -62,7 +62,8 @@ typedef enum {
     EFLA_ERR_WORKSPACE = 7,   /* workspace missing or smaller than the query said */
     EFLA_ERR_ALIGN = 8,       /* a pointer is not aligned as required */
     EFLA_ERR_TOO_LARGE = 9,   /* sizes need more than the fixed scratch of efla_chunk_fwd_noalloc */
-    EFLA_ERR_RULE = 10        /* unknown efla_rule */
+    EFLA_ERR_RULE = 10,       /* unknown efla_rule */
+    EFLA_ERR_OPTION = 11      /* unknown option, or a scalar argument out of its range */
 } efla_status;
 
 typedef enum {
@@ -356,6 +357,119 @@ efla_status efla_bwd_kept(const void *q, const void *k, const void *v, const voi
                           float *dkey, float *dval, float *dbeta, float *dS0, int B, int H, int L,
                           int dk, int dv, efla_dtype dt, efla_rule rule, const void *kept,
                           size_t kept_bytes, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Linear attention with a decay for each head.  The delta rule's siblings without its
+ * correction term (no counterpart on the pages): per head, for t = 1..L,
+ *
+ *   S_t = e^{l_t} S_{t-1} + k_t v_t^T,    o_t = S_t^T q_t.
+ *
+ * Layouts, state type, streams and errors are those of efla_chunk_fwd.  The log-decay l
+ * comes in one of two forms:
+ *   EFLA_DECAY_TOKEN -- [B,H,L] of type dt, one for every token
+ *   EFLA_DECAY_HEAD  -- [H] fp32, one for each head at every token
+ * l is expected to be <= 0 (not checked).  -inf forgets the state, so that a row can hold
+ * several documents: the first token of each carries l = -inf.  Values below -200 act as
+ * -inf (e^-200 is 0 in fp32); NaN propagates.
+ */
+typedef enum {
+    EFLA_DECAY_TOKEN = 0,
+    EFLA_DECAY_HEAD = 1
+} efla_decay_form;
+
+/*
+ * efla_decay_chunk_fwd -- the forward pass by chunks of 64 tokens: with c the running sum
+ * of l within a chunk that is entered with state S and leaves with c_C,
+ *   o_t = e^{c_t} S^T q_t + sum_{s<=t} e^{c_t - c_s} (q_t . k_s) v_s
+ *   S  <- e^{c_C} S + sum_s e^{c_C - c_s} k_s v_s^T.
+ *
+ *   q, k : [B,H,L,dk]  v : [B,H,L,dv] (dt)   S0 : [B,H,dk,dv] fp32 or NULL for zeros
+ *   o : [B,H,L,dv] (o_dt)   S_final : [B,H,dk,dv] fp32 or NULL; may be S0 (in-place carry)
+ *   workspace : efla_decay_chunk_fwd_workspace_size(...) bytes, 16-byte aligned, caller-owned
+ *       scratch (may be NULL when that is 0)
+ * Sizes: B,H >= 1, B*H <= 2^24, L >= 0, 1 <= dk,dv <= 128.  L == 0 copies S0 to S_final.
+ * Pointers are aligned to their element.  o must not alias an input.
+ */
+size_t efla_decay_chunk_fwd_workspace_size(int B, int H, int L, int dk, int dv, efla_dtype dt);
+efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, const void *log_g,
+                                 efla_decay_form form, const float *S0, void *o, float *S_final,
+                                 int B, int H, int L, int dk, int dv, efla_dtype dt,
+                                 efla_dtype o_dt, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/*
+ * efla_decay_bwd -- its gradients, given dO = dL/do ([B,H,L,dv], dt) and dS_final =
+ * dL/dS_final (fp32, or NULL for 0): dq, dkey [B,H,L,dk] and dval [B,H,L,dv] in dt, dlog_g
+ * = dL/dl ([B,H,L], dt) or NULL, dS0 (fp32) or NULL.  A token with l = -inf has dlog_g = 0.
+ * The per-head form is a constant of the model and has no gradient here: EFLA_ERR_OPTION
+ * where dlog_g is given with it.  The outputs must not alias an input or one another.
+ * workspace: efla_decay_bwd_workspace_size(...) bytes, 16-byte aligned.
+ */
+size_t efla_decay_bwd_workspace_size(int B, int H, int L, int dk, int dv, efla_dtype dt);
+efla_status efla_decay_bwd(const void *q, const void *k, const void *v, const void *log_g,
+                           efla_decay_form form, const float *S0, const void *dO,
+                           const float *dS_final, void *dq, void *dkey, void *dval, void *dlog_g,
+                           float *dS0, int B, int H, int L, int dk, int dv, efla_dtype dt,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * efla_decay_recurrent_step -- one decode token per head: S <- e^l S + k v^T in place, then
+ * o = S^T q.  q, k : [B,H,dk]  v : [B,H,dv] (dt); log_g : [B,H] (dt) or [H] fp32; S fp32,
+ * 16-byte aligned; o : [B,H,dv] (o_dt).  Sizes: 1 <= dk,dv <= 256.
+ */
+efla_status efla_decay_recurrent_step(const void *q, const void *k, const void *v,
+                                      const void *log_g, efla_decay_form form, float *S, void *o,
+                                      int B, int H, int dk, int dv, efla_dtype dt, efla_dtype o_dt,
+                                      void *stream);
+
+/*
+ * The norms around an attention of this library (which itself normalises nothing), with the
+ * change between the layout of the projections, [B,L,H,d], and that of the attention,
+ * [B,H,L,d].  A [B,L,H,d] input is a view given by its element strides {batch, token, head}
+ * with a dense last dimension, so that a slice of a fused projection needs no copy.
+ *
+ * efla_head_norm -- before it, for q or k:
+ *   y[b,h,t,:] = scale * w * x[b,t,h,:] / sqrt(m sum_i x_i^2 + eps),
+ *   m = 1 (EFLA_NORM_L2) or 1/d (EFLA_NORM_RMS);  y : [B,H,L,d].
+ * efla_gated_norm -- after it, for its output o ([B,H,L,d], o_dt):
+ *   y[b,t,h,:] = residual[b,t,h,:] + scale * act(gate[b,t,h,:]) * w * o[b,h,t,:] / sqrt(mean_i o_i^2 + eps),
+ *   act = x sigmoid(x) (EFLA_ACT_SILU) or sigmoid(x);  y : [B,L,H,d]; residual may be NULL
+ *   and, where it is dense, may be y.
+ * w is [d], dt or fp32 (w_dt), shared by the heads, or NULL for ones.  Arithmetic is fp32.
+ * The backward calls give dx / dgate dense in [B,L,H,d] (dt), d_o in [B,H,L,d] (o_dt) and,
+ * where dw is given, dw in w_dt, summed in a fixed order through workspace
+ * (efla_norm_bwd_workspace_size(d) bytes, 16-byte aligned; unused without dw).  dL/dresidual
+ * is dy itself.  Outputs must not alias an input otherwise.
+ * Sizes: B,L,H >= 0 (no rows is a no-op; dw is then 0), 1 <= d <= 256.  EFLA_ERR_OPTION: an
+ * unknown kind or act, or a scale or eps that is not finite, or eps < 0.  A row of zeros with
+ * eps = 0 gives NaN.
+ */
+typedef enum {
+    EFLA_NORM_L2 = 0,
+    EFLA_NORM_RMS = 1
+} efla_norm;
+typedef enum {
+    EFLA_ACT_SILU = 0,
+    EFLA_ACT_SIGMOID = 1
+} efla_act;
+size_t efla_norm_bwd_workspace_size(int d);
+efla_status efla_head_norm(const void *x, const long long *x_strides, const void *w,
+                           efla_dtype w_dt, void *y, int B, int L, int H, int d, efla_dtype dt,
+                           efla_norm kind, float scale, float eps, void *stream);
+efla_status efla_head_norm_bwd(const void *x, const long long *x_strides, const void *w,
+                               efla_dtype w_dt, const void *dy, void *dx, void *dw, int B, int L,
+                               int H, int d, efla_dtype dt, efla_norm kind, float scale, float eps,
+                               void *workspace, size_t workspace_bytes, void *stream);
+efla_status efla_gated_norm(const void *o, efla_dtype o_dt, const void *gate,
+                            const long long *gate_strides, const void *w, efla_dtype w_dt,
+                            const void *residual, const long long *residual_strides, void *y,
+                            int B, int L, int H, int d, efla_dtype dt, efla_act act, float scale,
+                            float eps, void *stream);
+efla_status efla_gated_norm_bwd(const void *o, efla_dtype o_dt, const void *gate,
+                                const long long *gate_strides, const void *w, efla_dtype w_dt,
+                                const void *dy, void *d_o, void *dgate, void *dw, int B, int L,
+                                int H, int d, efla_dtype dt, efla_act act, float scale, float eps,
+                                void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Reads and clears the library's device error word after synchronising
