@@ -7,6 +7,7 @@
 #include <atomic>
 
 #include "../../include/efla.h"
+#include "decay.h"
 #include "launchers.h"
 
 namespace efla {
@@ -302,11 +303,12 @@ unsigned long long efla_kernel_launches(void) {
 }
 
 efla_status efla_last_device_error(void *stream) {
-    unsigned int word = 0, bwd_word = 0;
+    unsigned int word = 0, bwd_word = 0, decay_word = 0;
     if (efla::tc_read_and_clear_error(&word, (cudaStream_t)stream) != cudaSuccess ||
-        efla::bwd_tc_read_and_clear_error(&bwd_word) != cudaSuccess)
+        efla::bwd_tc_read_and_clear_error(&bwd_word) != cudaSuccess ||
+        efla::decay::read_and_clear_error(&decay_word) != cudaSuccess)
         return EFLA_ERR_CUDA;
-    return (word | bwd_word) ? EFLA_ERR_TIMEOUT : EFLA_OK;
+    return (word | bwd_word | decay_word) ? EFLA_ERR_TIMEOUT : EFLA_OK;
 }
 
 }  // extern "C"

@@ -65,6 +65,15 @@ int simt_segments(int BH, int L, const int *blocks, int n);
 cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool in_bf16,
                               bool out_bf16, cudaStream_t s);
 
+// Tensor-core walks (decay_tc.cu): bf16 inputs, a and b of 64 or 128, x, y and z 16-byte aligned.  bwd: walks
+// with dots, given as DOT_PLANES shares (one for each warp of the output group); outputs are bf16.
+constexpr int DOT_PLANES = 4;
+bool tc_sizes(int dk, int dv, bool in_bf16);
+int tc_segments(int BH, int L, int n);
+cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out_bf16, bool bwd,
+                            cudaStream_t s);
+cudaError_t read_and_clear_error(unsigned int *out);
+
 // States of the segments: from every segment's own contribution (in seg, in walking order) and its
 // whole decay e^{sum l} (seg_e [BH][nseg]) to the state that enters it.
 cudaError_t launch_seg_chain(const Walks &ws, const float *seg_e, int BH, int nseg, cudaStream_t s);

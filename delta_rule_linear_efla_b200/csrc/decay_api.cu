@@ -42,10 +42,10 @@ struct Arena {
 int blocks_of(int b) { return (b + efla::decay::SIMT_BT - 1) / efla::decay::SIMT_BT; }
 
 // The walks' segments and their states: lays them out in the arena.
-int plan_segments(Walks &ws, int BH, int L, Arena &ar, float **seg_e) {
+int plan_segments(Walks &ws, int BH, int L, bool tc, Arena &ar, float **seg_e) {
     int blocks[efla::decay::MAX_WALKS];
     for (int i = 0; i < ws.n; ++i) blocks[i] = blocks_of(ws.w[i].b);
-    const int nseg = efla::decay::simt_segments(BH, L, blocks, ws.n);
+    const int nseg = tc ? efla::decay::tc_segments(BH, L, ws.n) : efla::decay::simt_segments(BH, L, blocks, ws.n);
     *seg_e = nullptr;
     if (nseg > 1) {
         for (int i = 0; i < ws.n; ++i) ws.w[i].seg = ar.floats((size_t)BH * nseg * ws.w[i].a * ws.w[i].b);
@@ -59,12 +59,12 @@ struct FwdPlan {
     float *seg_e = nullptr;
     int nseg = 1;
     size_t bytes = 0;
-    FwdPlan(int BH, int L, int dk, int dv, void *base) {
+    FwdPlan(int BH, int L, int dk, int dv, bool tc, void *base) {
         Arena ar{static_cast<char *>(base)};
         ws.n = 1;
         ws.w[0].a = dk;
         ws.w[0].b = dv;
-        nseg = plan_segments(ws, BH, L, ar, &seg_e);
+        nseg = plan_segments(ws, BH, L, tc, ar, &seg_e);
         bytes = ar.used;
     }
 };
@@ -72,22 +72,31 @@ struct FwdPlan {
 struct BwdPlan {
     Walks ws{};  // dq, dk, dv
     float *seg_e = nullptr, *S_end = nullptr, *dotq = nullptr, *dotk = nullptr;
-    int nseg = 1, nq = 1, nk = 1;
+    int nseg = 1, planes = 1;
     size_t bytes = 0;
-    BwdPlan(int BH, int L, int dk, int dv, void *base) {
+    BwdPlan(int BH, int L, int dk, int dv, bool tc, void *base) {
         Arena ar{static_cast<char *>(base)};
         ws.n = 3;
         ws.w[0].a = dv; ws.w[0].b = dk;
         ws.w[1].a = dv; ws.w[1].b = dk; ws.w[1].rev = 1;
         ws.w[2].a = dk; ws.w[2].b = dv; ws.w[2].rev = 1;
-        nq = nk = blocks_of(dk);
-        dotq = ar.floats((size_t)nq * BH * L);
-        dotk = ar.floats((size_t)nk * BH * L);
+        planes = tc ? efla::decay::DOT_PLANES : blocks_of(dk);
+        dotq = ar.floats((size_t)planes * BH * L);
+        dotk = ar.floats((size_t)planes * BH * L);
         S_end = ar.floats((size_t)BH * dk * dv);
-        nseg = plan_segments(ws, BH, L, ar, &seg_e);
+        nseg = plan_segments(ws, BH, L, tc, ar, &seg_e);
         bytes = ar.used;
     }
 };
+
+// The workspace of either path: which one runs also depends on the pointers' alignment.
+template <typename Plan>
+size_t plan_bytes(int BH, int L, int dk, int dv, bool bf16) {
+    const size_t n = Plan(BH, L, dk, dv, false, nullptr).bytes;
+    if (!efla::decay::tc_sizes(dk, dv, bf16)) return n;
+    const size_t t = Plan(BH, L, dk, dv, true, nullptr).bytes;
+    return n > t ? n : t;
+}
 
 }  // namespace
 
@@ -95,7 +104,7 @@ extern "C" {
 
 size_t efla_decay_chunk_fwd_workspace_size(int B, int H, int L, int dk, int dv, efla_dtype dt) {
     if (!dtype_ok(dt) || !sizes_ok(B, H, L, dk, dv) || L == 0 || dk > 128 || dv > 128) return 0;
-    return FwdPlan(B * H, L, dk, dv, nullptr).bytes;
+    return plan_bytes<FwdPlan>(B * H, L, dk, dv, dt == EFLA_BF16);
 }
 
 efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, const void *log_g,
@@ -118,21 +127,24 @@ efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, co
         return from_cuda(S0 ? cudaMemcpyAsync(S_final, S0, state, cudaMemcpyDeviceToDevice, s)
                             : cudaMemsetAsync(S_final, 0, state, s));
     }
-    FwdPlan p(BH, L, dk, dv, workspace);
-    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes)) return EFLA_ERR_WORKSPACE;
+    const size_t need = efla_decay_chunk_fwd_workspace_size(B, H, L, dk, dv, dt);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+    const bool tc = efla::decay::tc_sizes(dk, dv, dt == EFLA_BF16) && aligned(q, 16) && aligned(k, 16) && aligned(v, 16);
+    FwdPlan p(BH, L, dk, dv, tc, workspace);
     Walk &w = p.ws.w[0];
     w.x = q; w.y = k; w.z = v;
     w.s0 = S0;
     w.out = o;
     w.s_end = S_final;
     const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
+    if (tc) return from_cuda(efla::decay::launch_walks_tc(p.ws, g, BH, L, p.nseg, p.seg_e, o_dt == EFLA_BF16, false, s));
     return from_cuda(efla::decay::launch_walks_simt(p.ws, g, BH, L, p.nseg, p.seg_e, dt == EFLA_BF16,
                                                     o_dt == EFLA_BF16, s));
 }
 
 size_t efla_decay_bwd_workspace_size(int B, int H, int L, int dk, int dv, efla_dtype dt) {
     if (!dtype_ok(dt) || !sizes_ok(B, H, L, dk, dv) || L == 0 || dk > 128 || dv > 128) return 0;
-    return BwdPlan(B * H, L, dk, dv, nullptr).bytes;
+    return plan_bytes<BwdPlan>(B * H, L, dk, dv, dt == EFLA_BF16);
 }
 
 efla_status efla_decay_bwd(const void *q, const void *k, const void *v, const void *log_g, efla_decay_form form,
@@ -158,8 +170,10 @@ efla_status efla_decay_bwd(const void *q, const void *k, const void *v, const vo
         return from_cuda(dS_final ? cudaMemcpyAsync(dS0, dS_final, state, cudaMemcpyDeviceToDevice, s)
                                   : cudaMemsetAsync(dS0, 0, state, s));
     }
-    BwdPlan p(BH, L, dk, dv, workspace);
-    if (!workspace || workspace_bytes < p.bytes) return EFLA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < efla_decay_bwd_workspace_size(B, H, L, dk, dv, dt)) return EFLA_ERR_WORKSPACE;
+    const bool tc = efla::decay::tc_sizes(dk, dv, dt == EFLA_BF16) && aligned(q, 16) && aligned(k, 16) && aligned(v, 16) &&
+                    aligned(dO, 16);
+    BwdPlan p(BH, L, dk, dv, tc, workspace);
     const bool want_dl = dlog_g != nullptr, tail = want_dl && dS_final;
     Walk &a = p.ws.w[0], &b = p.ws.w[1], &c = p.ws.w[2];
     a.x = dO; a.y = v; a.z = k;
@@ -178,9 +192,11 @@ efla_status efla_decay_bwd(const void *q, const void *k, const void *v, const vo
         b.dotx = k; b.dot = p.dotk;
     }
     const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
-    cudaError_t e = efla::decay::launch_walks_simt(p.ws, g, BH, L, p.nseg, p.seg_e, dt == EFLA_BF16, dt == EFLA_BF16, s);
+    const bool bf16 = dt == EFLA_BF16;
+    const cudaError_t e = tc ? efla::decay::launch_walks_tc(p.ws, g, BH, L, p.nseg, p.seg_e, bf16, true, s)
+                             : efla::decay::launch_walks_simt(p.ws, g, BH, L, p.nseg, p.seg_e, bf16, bf16, s);
     if (e != cudaSuccess || !want_dl) return from_cuda(e);
-    return from_cuda(efla::decay::launch_dlog(p.dotq, p.nq, p.dotk, p.nk, dS_final, tail ? p.S_end : nullptr, g, dlog_g,
+    return from_cuda(efla::decay::launch_dlog(p.dotq, p.planes, p.dotk, p.planes, dS_final, tail ? p.S_end : nullptr, g, dlog_g,
                                               BH, L, dk, dv, s));
 }
 

@@ -1,0 +1,556 @@
+// decay_tc.cu -- linear attention with a decay for each head on the tensor cores (tcgen05, TMEM, TMA):
+// the walks of decay.h for bf16 inputs with a and b of 64 or 128.
+//
+// One CTA walks one stretch of one head, a chunk of 64 tokens at a time.  The state and value
+// dimensions are the MMA's M, so that the state stays in tensor memory as S^T, fp32, and its 16-bit copy
+// is a tensor-memory operand:
+//
+//   P        = X Y^T                        [64 x 64]
+//   O2^T     = Z^T (D o P)^T                [b x 64]
+//   O1^T     = S^T X^T                      [b x 64]     out = diag(q) O1 + O2
+//   S^T      = e^{c_C} S^T + Z^T Yw         [b x a]      Yw = diag(w) Y
+//
+// What is rounded to bf16 on the way, and how often:
+//   D o P   once: 2^-9 of terms that add like the bf16 output itself.
+//   Yw      as two bf16 halves (Yw = hi + lo to 2^-17), two products into the fp32 state: the state is an
+//           fp32 result, and a sequence's rounding errors would gather in it.
+//   S^T     once for o and for dv.  For dq and dk, whose dots with q and k give dl, as two halves: dl is
+//           a suffix sum of q.dq - k.dk that cancels down to the pairs that straddle a token; errors of
+//           D o P cancel with them (dq and dk round the same products), errors of two different state
+//           copies would not, and would grow with the square root of the sequence.
+// Decay factors and the sums over them are fp32 (their logarithms' sums fp64, decay_gate.cuh).
+//
+// Warp roles (one CTA an SM, 19 warps):
+//   0-3   weight:  Yw's halves from Y's tile
+//   4-7   mask:    D o P from TMEM into its operand tile
+//   8-11  state:   S^T after a chunk: its 16-bit copy, and scaled by the next chunk's e^{c_C}
+//   12-15 output:  out^T from TMEM to global memory, and its dots
+//   16    MMA issuer   17 TMA producer   18 decays (sums and weights, up to four chunks ahead)
+// Every mbarrier wait is bounded; a wait that gives up sets the device error word, lets what is in flight
+// land (again bounded), frees its tensor memory and exits.
+#include <cudaTypedefs.h>
+
+#include "decay_gate.cuh"
+#include "launchers.h"
+#include "tc_ptx.cuh"
+#include "tmap.h"
+
+namespace efla {
+namespace decay {
+
+static __device__ unsigned int g_decay_error = 0;
+
+namespace {
+
+constexpr int WARPS = 19, THREADS = WARPS * 32;
+constexpr int W_MMA = 16, W_TMA = 17, W_GATE = 18;
+constexpr int NS = 3;     // stages of X, Y, Z
+constexpr int SLOTS = 4;  // chunks of decay weights
+constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
+
+struct Maps {
+    CUtensorMap x[MAX_WALKS], y[MAX_WALKS], z[MAX_WALKS];
+};
+
+template <int A, int B, bool BWD>
+struct Cfg {
+    static constexpr int XB = (A / 64) * 8192, ZB = (B / 64) * 8192;
+    static constexpr int OFF_X = 0, OFF_Y = XB, OFF_Z = 2 * XB, STAGE = 2 * XB + ZB;
+    static constexpr int OFF_W = NS * STAGE;        // Yw: two buffers of [hi | lo]
+    static constexpr int OFF_P = OFF_W + 4 * XB;    // D o P
+    static constexpr int SMEM = OFF_P + 8192 + 1024;  // + alignment slack
+    // tensor memory columns
+    static constexpr int NB = BWD && A == 128 ? 1 : 2;  // buffers of O1^T and O2^T
+    static constexpr uint32_t T_S = 0, T_H = A, T_L = T_H + A / 2, T_P = T_L + (BWD ? A / 2 : 0), T_O = T_P + 64;
+    static_assert(T_O + NB * 128 <= 512, "tensor memory");
+};
+
+struct Bars {
+    // one arrival (a commit, a thread, or a TMA load)
+    uint64_t full[NS], free_s[NS], gready[SLOTS], y_free[2], pdone, d1done, d2done, odone[2], drain;
+    // one arrival from each of four warps
+    uint64_t gfree[SLOTS], y_ready[2], p_ready, s_ready, o_free[2];
+};
+constexpr int BARS_ONE = 2 * NS + SLOTS + 2 + 3 + 2 + 1;
+
+struct Slot {
+    float qw[C], kw[C];
+    float2 c2[C];  // running sum in units of log 2, hi and lo
+    float tot, pad[3];
+};
+
+template <int M>
+__device__ __forceinline__ int acc_row(int warp, int lane) {
+    if constexpr (M == 128) return 32 * warp + lane;
+    else return lane < 16 ? 16 * warp + lane : -1;
+}
+
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+    tc::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// Two floats as packed bf16 halves: x = hi + lo to 2^-17 of |x|.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = tc::pack_bf16(x, y);
+    lo = tc::pack_bf16(x - bf_lo(hi), y - bf_hi(hi));
+}
+
+// The sums over a warp's lanes of 32 columns: lane l ends with column l's.
+__device__ __forceinline__ float column_sums(float (&p)[32], int lane) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const bool up = lane & off;
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const float keep = up ? p[i + off] : p[i], send = up ? p[i] : p[i + off];
+            p[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    }
+    return p[0];
+}
+
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// OUT = false: the stretch's own contribution to the state only (the segments' first pass).  BWD: walks
+// that may have dots (w.dot), with the state's copy in two halves where they do.
+template <int A, int B, typename TO, bool OUT, bool BWD>
+__global__ void __launch_bounds__(THREADS, 1)
+    walk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Walks ws, const Gate g, int BH, int L,
+                   int nseg, int seg_chunks, float *__restrict__ seg_e) {
+    using K = Cfg<A, B, BWD>;
+    constexpr int NB = K::NB;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_u32 = tc::smem_u32(smem_raw);
+    uint8_t *base = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
+    __shared__ Bars bars;
+    __shared__ __align__(16) Slot slots[SLOTS];
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int abort_flag;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, gtid = tid & 127;
+    // ---- blockIdx.x = (head, segment in walking order, walk)
+    const int wi = blockIdx.x % ws.n, rest = blockIdx.x / ws.n;
+    const int segs = OUT ? nseg : nseg - 1;
+    const int seg = rest % segs, bh = rest / segs;
+    const Walk &w = ws.w[wi];
+    const bool rev = w.rev != 0, split = BWD && w.dot != nullptr;
+    const int NC = (L + C - 1) / C;
+    const int i0 = seg * seg_chunks, cnt = min(NC, i0 + seg_chunks) - i0;
+    auto chunk = [&](int i) { return rev ? NC - 1 - (i0 + i) : i0 + i; };
+
+    if (tid == 0) {
+        uint64_t *b = reinterpret_cast<uint64_t *>(&bars);
+        for (int i = 0; i < (int)(sizeof(Bars) / sizeof(uint64_t)); ++i) tc::mbar_init(b + i, i < BARS_ONE ? 1 : 4);
+        tc::fence_mbar_init();
+        abort_flag = 0;
+        tc::tma_prefetch_desc(&maps.x[wi]);
+        tc::tma_prefetch_desc(&maps.y[wi]);
+        tc::tma_prefetch_desc(&maps.z[wi]);
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(&tmem_base, 512);
+        tc::tmem_relinquish();
+    }
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_base, lane_base = (uint32_t)(32 * (warp & 3)) << 16, sb = tc::smem_u32(base);
+    const long long budget = WAIT_BUDGET;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        return tc::mbar_wait_or_abort(bar, parity & 1, &abort_flag, budget);
+    };
+    auto wait_gate = [&](int n) { return wait(&bars.gready[n % SLOTS], n / SLOTS); };
+
+    if (warp == W_TMA) {
+        if (lane == 0) {
+            int n = 0;
+            for (; n < cnt; ++n) {
+                const int st = n % NS, c0 = chunk(n) * C;
+                if (n >= NS && !wait(&bars.free_s[st], n / NS - 1)) break;
+                uint8_t *s = base + st * K::STAGE;
+                tc::mbar_expect_tx(&bars.full[st], (OUT ? 2 : 1) * K::XB + K::ZB);
+#pragma unroll
+                for (int j = 0; j < A / 64; ++j) {
+                    if (OUT) tc::tma_load_3d(s + K::OFF_X + j * 8192, &maps.x[wi], &bars.full[st], j * 64, c0, bh);
+                    tc::tma_load_3d(s + K::OFF_Y + j * 8192, &maps.y[wi], &bars.full[st], j * 64, c0, bh);
+                }
+#pragma unroll
+                for (int j = 0; j < B / 64; ++j)
+                    tc::tma_load_3d(s + K::OFF_Z + j * 8192, &maps.z[wi], &bars.full[st], j * 64, c0, bh);
+            }
+            if (abort_flag)  // let this CTA's own copies land before it exits (bounded)
+                for (int m = n > NS ? n - NS : 0; m < n; ++m) tc::mbar_wait(&bars.full[m % NS], (m / NS) & 1, budget / 8);
+        }
+    } else if (warp == W_MMA) {
+        if (lane == 0) {
+            constexpr uint32_t id_p = tc::idesc_bf16(64, 64, false, false);
+            constexpr uint32_t id_o1 = tc::idesc_bf16(B, 64, false, false);
+            constexpr uint32_t id_o2 = tc::idesc_bf16(B, 64, true, false);
+            constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true);
+            auto issue_p = [&](int n) {
+                const uint32_t s = sb + (n % NS) * K::STAGE;
+#pragma unroll
+                for (int kk = 0; kk < A / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * 8192 + (kk & 3) * 32;
+                    tc::mma_bf16(tmem + K::T_P, tc::sdesc(s + K::OFF_X + off, 16, 1024), tc::sdesc(s + K::OFF_Y + off, 16, 1024),
+                                 id_p, kk > 0);
+                }
+                tc::mma_commit(&bars.pdone);
+            };
+            bool issued = false, ok = true;
+            if (OUT) {
+                ok = wait(&bars.full[0], 0);
+                if (ok) {
+                    issued = true;
+                    issue_p(0);
+                }
+            }
+            for (int n = 0; ok && n < cnt; ++n) {
+                const uint32_t s = sb + (n % NS) * K::STAGE, z = s + K::OFF_Z, x = s + K::OFF_X;
+                const uint32_t yw = sb + K::OFF_W + (n & 1) * 2 * K::XB;
+                // S^T += Z^T Yw
+                if (!OUT && !wait(&bars.full[n % NS], n / NS)) break;
+                if (!wait(&bars.y_ready[n & 1], n >> 1) || !wait(&bars.s_ready, n)) break;
+                tc::tc_fence_after();
+                issued = true;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_bf16(tmem + K::T_S, tc::sdesc(z + kk * 2048, 8192, 1024),
+                                     tc::sdesc(yw + h * K::XB + kk * 2048, 8192, 1024), id_s, 1u);
+                tc::mma_commit(&bars.d2done);
+                tc::mma_commit(&bars.y_free[n & 1]);
+                if (OUT) {
+                    const int ob = n % NB;
+                    const uint32_t o1 = tmem + K::T_O + ob * 128, o2 = o1 + 64;
+                    if (n >= NB && !wait(&bars.o_free[ob], n / NB - 1)) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < A / 16; ++kk)
+                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, tc::sdesc(x + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
+                                       id_o1, kk > 0);
+                    if (BWD && split) {
+#pragma unroll
+                        for (int kk = 0; kk < A / 16; ++kk)
+                            tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8, tc::sdesc(x + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
+                                           id_o1, 1u);
+                    }
+                    tc::mma_commit(&bars.d1done);
+                    if (!wait(&bars.p_ready, n)) break;
+                    tc::tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc::mma_bf16(o2, tc::sdesc(z + kk * 2048, 8192, 1024), tc::sdesc(sb + K::OFF_P + kk * 32, 16, 1024),
+                                     id_o2, kk > 0);
+                    tc::mma_commit(&bars.odone[ob]);
+                }
+                tc::mma_commit(&bars.free_s[n % NS]);
+                if (OUT && n + 1 < cnt) {
+                    if (!wait(&bars.full[(n + 1) % NS], (n + 1) / NS)) break;
+                    issue_p(n + 1);
+                }
+            }
+            if (issued) {  // nothing of this CTA's is in flight when it exits (bounded)
+                tc::mma_commit(&bars.drain);
+                tc::mbar_wait(&bars.drain, 0, budget / 4);
+            }
+        }
+    } else if (warp == W_GATE) {
+        double sum = 0.0;
+        for (int n = 0; n < cnt; ++n) {
+            const PairSum c = chunk_sums(g, bh, L, chunk(n) * C, lane);
+            const double cC = __shfl_sync(0xffffffffu, c.c1, 31), cc[2] = {c.c0, c.c1};
+            sum += cC;
+            if (n >= SLOTS && !wait(&bars.gfree[n % SLOTS], n / SLOTS - 1)) break;
+            Slot &sl = slots[n % SLOTS];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int t = 2 * lane + e;
+                const float up = exp_sum(cc[e]), down = exp_sum(cC - cc[e]);
+                sl.qw[t] = rev ? down : up;
+                sl.kw[t] = rev ? up : down;
+                const double c2 = cc[e] * 1.4426950408889634;
+                sl.c2[t] = make_float2((float)c2, (float)(c2 - (double)(float)c2));
+            }
+            if (lane == 0) sl.tot = exp_sum(cC);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars.gready[n % SLOTS]);
+        }
+        // every walk in the same direction finds the same decay of a segment: its first one writes it
+        if (!OUT && lane == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
+            seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp_sum(sum);
+    } else if (wg == 0) {
+        // ---------------------------------------------------------- Yw
+        for (int n = 0; n < cnt; ++n) {
+            if (!wait_gate(n) || !wait(&bars.full[n % NS], n / NS)) break;
+            if (n >= 2 && !wait(&bars.y_free[n & 1], (n >> 1) - 1)) break;
+            const uint4 *y = reinterpret_cast<const uint4 *>(base + (n % NS) * K::STAGE + K::OFF_Y);
+            uint4 *hi = reinterpret_cast<uint4 *>(base + K::OFF_W + (n & 1) * 2 * K::XB);
+            uint4 *lo = hi + K::XB / 16;
+            const float *kw = slots[n % SLOTS].kw;
+#pragma unroll
+            for (int i = gtid; i < K::XB / 16; i += 128) {  // 8 pieces of 16 bytes a row of a 64-column slab
+                const float f = kw[(i >> 3) & 63];
+                const uint4 u = y[i];
+                uint4 h, l;
+                split2(f * bf_lo(u.x), f * bf_hi(u.x), h.x, l.x);
+                split2(f * bf_lo(u.y), f * bf_hi(u.y), h.y, l.y);
+                split2(f * bf_lo(u.z), f * bf_hi(u.z), h.z, l.z);
+                split2(f * bf_lo(u.w), f * bf_hi(u.w), h.w, l.w);
+                hi[i] = h;
+                lo[i] = l;
+            }
+            tc::fence_async_smem();
+            warp_arrive(&bars.y_ready[n & 1], lane);
+        }
+    } else if (wg == 1) {
+        // ---------------------------------------------------------- D o P
+        const int r = acc_row<64>(warp & 3, lane);
+        uint8_t *pt = base + K::OFF_P;
+        for (int n = 0; OUT && n < cnt; ++n) {
+            if (!wait_gate(n) || !wait(&bars.pdone, n)) break;
+            tc::tc_fence_after();
+            const Slot &sl = slots[n % SLOTS];
+            const float2 cr = sl.c2[r < 0 ? 0 : r];
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb) {
+                float v[32];
+                tc::tmem_ld32(tmem + lane_base + K::T_P + hb * 32, v);
+                if (r >= 0) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float4 cc = *reinterpret_cast<const float4 *>(&sl.c2[hb * 32 + j]);
+                        const int c0 = hb * 32 + j;
+                        const float d0 = (cr.x - cc.x) + (cr.y - cc.y), d1 = (cr.x - cc.z) + (cr.y - cc.w);
+                        const bool on0 = rev ? c0 >= r : c0 <= r, on1 = rev ? c0 + 1 >= r : c0 + 1 <= r;
+                        v[j] = on0 ? v[j] * ex2(rev ? -d0 : d0) : 0.f;
+                        v[j + 1] = on1 ? v[j + 1] * ex2(rev ? -d1 : d1) : 0.f;
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r, hb * 4 + c)) =
+                            make_uint4(tc::pack_bf16(v[8 * c], v[8 * c + 1]), tc::pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                                       tc::pack_bf16(v[8 * c + 4], v[8 * c + 5]), tc::pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+                }
+            }
+            tc::fence_async_smem();
+            warp_arrive(&bars.p_ready, lane);
+        }
+    } else if (wg == 2) {
+        // ---------------------------------------------------------- S^T
+        const int j = acc_row<B>(warp & 3, lane);
+        const size_t ab = (size_t)A * B;
+        const float *sin = nullptr;
+        if (OUT) sin = nseg > 1 ? w.seg + ((size_t)bh * nseg + seg) * ab : (w.s0 ? w.s0 + bh * ab : nullptr);
+        const bool st = nseg == 1 && w.s0_t;
+        bool ok = true;
+        for (int n = 0; ok && n < cnt; ++n) {
+            ok = wait_gate(n) && (n == 0 || wait(&bars.d2done, n - 1));
+            if (!ok) break;
+            tc::tc_fence_after();
+            if (!OUT && n > 0) {  // the weights of the chunk before are read (its Yw was)
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.gfree[(n - 1) % SLOTS]);
+            }
+            const float tot = slots[n % SLOTS].tot;
+#pragma unroll
+            for (int cb = 0; cb < A / 32; ++cb) {
+                float v[32];
+                if (n > 0) {
+                    tc::tmem_ld32(tmem + lane_base + K::T_S + cb * 32, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = sin && j >= 0 ? (st ? sin[(size_t)j * A + cb * 32 + i] : sin[(size_t)(cb * 32 + i) * B + j]) : 0.f;
+                }
+                if (OUT) {
+                    if (cb == 0 && n > 0) {  // the copy's last reader
+                        ok = wait(&bars.d1done, n - 1);
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                    }
+                    uint32_t h[16], l[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+                    tc::tmem_st16u(tmem + lane_base + K::T_H + cb * 16, h);
+                    if (BWD && split) tc::tmem_st16u(tmem + lane_base + K::T_L + cb * 16, l);
+                }
+                uint32_t u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * tot);
+                tc::tmem_st32u(tmem + lane_base + K::T_S + cb * 32, u);
+            }
+            if (!ok) break;
+            warp_arrive(&bars.s_ready, lane);
+        }
+        float *sout = nullptr;
+        if (!OUT) sout = w.seg + ((size_t)bh * nseg + seg) * ab;
+        else if (seg == nseg - 1 && w.s_end) sout = w.s_end + bh * ab;
+        if (ok && sout && wait(&bars.d2done, cnt - 1)) {
+            tc::tc_fence_after();
+#pragma unroll
+            for (int cb = 0; cb < A / 32; ++cb) {
+                float v[32];
+                tc::tmem_ld32(tmem + lane_base + K::T_S + cb * 32, v);
+                if (j >= 0)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) sout[(size_t)(cb * 32 + i) * B + j] = v[i];
+            }
+        }
+    } else if (OUT && wg == 3) {
+        // ---------------------------------------------------------- out
+        const int j = acc_row<B>(warp & 3, lane);
+        TO *out = static_cast<TO *>(w.out);
+        const __nv_bfloat16 *dx = static_cast<const __nv_bfloat16 *>(w.dotx);
+        for (int n = 0; n < cnt; ++n) {
+            const int t0 = chunk(n) * C, cl = min(C, L - t0), ob = n % NB;
+            const size_t row0 = (size_t)bh * L + t0;
+            uint32_t xr[32];  // this lane's elements of the dots' other factor, two tokens a word
+            if (BWD && split) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const unsigned short *p = reinterpret_cast<const unsigned short *>(dx) + (row0 + 2 * i) * B + j;
+                    const uint32_t a = j >= 0 && 2 * i < cl ? p[0] : 0, b = j >= 0 && 2 * i + 1 < cl ? p[B] : 0;
+                    xr[i] = a | (b << 16);
+                }
+            }
+            if (!wait_gate(n) || !wait(&bars.odone[ob], n / NB)) break;
+            tc::tc_fence_after();
+            const float *qw = slots[n % SLOTS].qw;
+            const uint32_t o1 = tmem + lane_base + K::T_O + ob * 128;
+#pragma unroll
+            for (int hb = 0; hb < 2; ++hb) {
+                float v[32];
+                tc::tmem_ld32(o1 + hb * 32, v);
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(qw + hb * 32 + i);
+                    v[i] *= f.x; v[i + 1] *= f.y; v[i + 2] *= f.z; v[i + 3] *= f.w;
+                }
+#pragma unroll
+                for (int qb = 0; qb < 2; ++qb) {
+                    float u[16];
+                    tc::tmem_ld16(o1 + 64 + hb * 32 + qb * 16, u);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[qb * 16 + i] += u[i];
+                }
+                if (hb == 1) {
+                    warp_arrive(&bars.o_free[ob], lane);
+                    if (lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
+                }
+                if (j >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (hb * 32 + i < cl) put(out + (row0 + hb * 32 + i) * B + j, v[i]);
+                }
+                if (BWD && split) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        v[2 * i] = j >= 0 ? v[2 * i] * bf_lo(xr[hb * 16 + i]) : 0.f;
+                        v[2 * i + 1] = j >= 0 ? v[2 * i + 1] * bf_hi(xr[hb * 16 + i]) : 0.f;
+                    }
+                    const float s = column_sums(v, lane);
+                    if (hb * 32 + lane < cl) w.dot[((size_t)(warp & 3) * BH + bh) * L + t0 + hb * 32 + lane] = s;
+                }
+            }
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && abort_flag) atomicOr(&g_decay_error, 1u);
+    if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+template <int A, int B, typename TO, bool BWD>
+cudaError_t launch_t(const Maps &maps, const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out,
+                     cudaStream_t s) {
+    const int NC = (L + C - 1) / C, per = (NC + nseg - 1) / nseg;
+    constexpr int smem = Cfg<A, B, BWD>::SMEM;
+    auto *kernel = out ? walk_tc_kernel<A, B, TO, true, BWD> : walk_tc_kernel<A, B, TO, false, BWD>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)BH * (out ? nseg : nseg - 1) * ws.n, THREADS, smem, s>>>(maps, ws, g, BH, L, nseg, per, seg_e);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <typename TO, bool BWD>
+cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out, cudaStream_t s) {
+    Maps maps;
+    for (int i = 0; i < ws.n; ++i) {
+        const Walk &w = ws.w[i];
+        if (!tmap::make_3d(&maps.x[i], w.x, w.a, L, BH, 64, C) || !tmap::make_3d(&maps.y[i], w.y, w.a, L, BH, 64, C) ||
+            !tmap::make_3d(&maps.z[i], w.z, w.b, L, BH, 64, C))
+            return cudaErrorInvalidValue;
+    }
+    const int a = ws.w[0].a, b = ws.w[0].b;
+    if (a == 128 && b == 128) return launch_t<128, 128, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
+    if (a == 128) return launch_t<128, 64, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
+    if (b == 128) return launch_t<64, 128, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
+    return launch_t<64, 64, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
+}
+
+cudaError_t launch_pass(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out_bf16, bool bwd, bool out,
+                        cudaStream_t s) {
+    // walks of the same head sizes share a launch
+    Walks part{};
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < ws.n && e == cudaSuccess; ++i) {
+        part.w[part.n++] = ws.w[i];
+        if (i + 1 < ws.n && ws.w[i + 1].a == ws.w[i].a && ws.w[i + 1].b == ws.w[i].b) continue;
+        if (bwd) e = launch_ab<__nv_bfloat16, true>(part, g, BH, L, nseg, seg_e, out, s);
+        else if (out_bf16) e = launch_ab<__nv_bfloat16, false>(part, g, BH, L, nseg, seg_e, out, s);
+        else e = launch_ab<float, false>(part, g, BH, L, nseg, seg_e, out, s);
+        part.n = 0;
+    }
+    return e;
+}
+
+}  // namespace
+
+bool tc_sizes(int dk, int dv, bool bf16) { return bf16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
+
+int tc_segments(int BH, int L, int n) {
+    // One CTA an SM.  Cutting a sequence costs a first pass (the state update alone), so it is cut only
+    // as far as its CTAs still fit the device at once, at four chunks a segment or more.
+    const long long units = (long long)BH * n;
+    const int NC = (L + C - 1) / C;
+    long long want = 148 / units;
+    if (want > NC / 4) want = NC / 4;
+    if (want < 2) return 1;
+    const int per = (int)((NC + want - 1) / want);
+    return (NC + per - 1) / per;
+}
+
+cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out_bf16, bool bwd,
+                            cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (nseg > 1) {
+        e = launch_pass(ws, g, BH, L, nseg, seg_e, out_bf16, bwd, false, s);
+        if (e == cudaSuccess) e = launch_seg_chain(ws, seg_e, BH, nseg, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pass(ws, g, BH, L, nseg, seg_e, out_bf16, bwd, true, s);
+}
+
+cudaError_t read_and_clear_error(unsigned int *out) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_decay_error, sizeof(unsigned int));
+    if (e != cudaSuccess || *out == 0) return e;
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_decay_error, &zero, sizeof(unsigned int));
+}
+
+}  // namespace decay
+}  // namespace efla
