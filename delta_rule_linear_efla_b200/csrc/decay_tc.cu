@@ -91,6 +91,39 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     if (lane == 0) tc::mbar_arrive(bar);
 }
 
+// Bounded wait that also gives up once another role has.  The try_wait carries a suspend-time hint (as a
+// kernel of 19 warps that mostly wait must): without one the waiting warps' polls took four of five issue
+// slots from the working ones (a chunk took 8800 cycles).
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    const uint32_t addr = tc::smem_u32(bar);
+    long long t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        const long long t = clock64();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > WAIT_BUDGET) {
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -167,9 +200,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc::tc_fence_after();
     const uint32_t tmem = tmem_base, lane_base = (uint32_t)(32 * (warp & 3)) << 16, sb = tc::smem_u32(base);
     const long long budget = WAIT_BUDGET;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return tc::mbar_wait_or_abort(bar, parity & 1, &abort_flag, budget);
-    };
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity & 1, &abort_flag); };
     auto wait_gate = [&](int n) { return wait(&bars.gready[n % SLOTS], n / SLOTS); };
 
     if (warp == W_TMA) {
@@ -193,79 +224,96 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int m = n > NS ? n - NS : 0; m < n; ++m) tc::mbar_wait(&bars.full[m % NS], (m / NS) & 1, budget / 8);
         }
     } else if (warp == W_MMA) {
-        if (lane == 0) {
-            constexpr uint32_t id_p = tc::idesc_bf16(64, 64, false, false);
-            constexpr uint32_t id_o1 = tc::idesc_bf16(B, 64, false, false);
-            constexpr uint32_t id_o2 = tc::idesc_bf16(B, 64, true, false);
-            constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true);
-            auto issue_p = [&](int n) {
-                const uint32_t s = sb + (n % NS) * K::STAGE;
+        // The whole warp runs the loop and one elected lane issues, so that descriptors are warp-uniform.
+        constexpr uint32_t id_p = tc::idesc_bf16(64, 64, false, false);
+        constexpr uint32_t id_o1 = tc::idesc_bf16(B, 64, false, false);
+        constexpr uint32_t id_o2 = tc::idesc_bf16(B, 64, true, false);
+        constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true);
+        // descriptors of the first stage / buffer; others are their distance / 16 further on
+        const uint64_t dx = tc::sdesc(sb + K::OFF_X, 16, 1024), dy = tc::sdesc(sb + K::OFF_Y, 16, 1024);
+        const uint64_t dz = tc::sdesc(sb + K::OFF_Z, 8192, 1024), dw = tc::sdesc(sb + K::OFF_W, 8192, 1024);
+        const uint64_t dp = tc::sdesc(sb + K::OFF_P, 16, 1024);
+        const bool leader = elect();
+        auto issue_p = [&](int st) {
+            if (leader) {
+                const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
 #pragma unroll
                 for (int kk = 0; kk < A / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * 8192 + (kk & 3) * 32;
-                    tc::mma_bf16(tmem + K::T_P, tc::sdesc(s + K::OFF_X + off, 16, 1024), tc::sdesc(s + K::OFF_Y + off, 16, 1024),
-                                 id_p, kk > 0);
+                    const uint32_t off = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
+                    tc::mma_bf16(tmem + K::T_P, dx + o + off, dy + o + off, id_p, kk > 0);
                 }
                 tc::mma_commit(&bars.pdone);
-            };
-            bool issued = false, ok = true;
-            if (OUT) {
-                ok = wait(&bars.full[0], 0);
-                if (ok) {
-                    issued = true;
-                    issue_p(0);
-                }
             }
-            for (int n = 0; ok && n < cnt; ++n) {
-                const uint32_t s = sb + (n % NS) * K::STAGE, z = s + K::OFF_Z, x = s + K::OFF_X;
-                const uint32_t yw = sb + K::OFF_W + (n & 1) * 2 * K::XB;
-                // S^T += Z^T Yw
-                if (!OUT && !wait(&bars.full[n % NS], n / NS)) break;
-                if (!wait(&bars.y_ready[n & 1], n >> 1) || !wait(&bars.s_ready, n)) break;
-                tc::tc_fence_after();
+            __syncwarp();
+        };
+        bool issued = false, ok = true;
+        if (OUT) {
+            ok = wait(&bars.full[0], 0);
+            if (ok) {
                 issued = true;
+                issue_p(0);
+            }
+        }
+        int st = 0, ph = 0;  // stage and its pass
+        for (int n = 0; ok && n < cnt; ++n) {
+            const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
+            // S^T += Z^T Yw
+            if (!OUT && !wait(&bars.full[st], ph)) break;
+            if (!wait(&bars.y_ready[n & 1], n >> 1) || !wait(&bars.s_ready, n)) break;
+            tc::tc_fence_after();
+            issued = true;
+            if (leader) {
+                const uint64_t yw = dw + (uint64_t)((n & 1) * (2 * K::XB >> 4));
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_bf16(tmem + K::T_S, tc::sdesc(z + kk * 2048, 8192, 1024),
-                                     tc::sdesc(yw + h * K::XB + kk * 2048, 8192, 1024), id_s, 1u);
+                        tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + (h * (K::XB >> 4) + kk * 128), id_s, 1u);
                 tc::mma_commit(&bars.d2done);
                 tc::mma_commit(&bars.y_free[n & 1]);
-                if (OUT) {
-                    const int ob = n % NB;
-                    const uint32_t o1 = tmem + K::T_O + ob * 128, o2 = o1 + 64;
-                    if (n >= NB && !wait(&bars.o_free[ob], n / NB - 1)) break;
-                    tc::tc_fence_after();
+            }
+            __syncwarp();
+            if (OUT) {
+                const int ob = n % NB;
+                const uint32_t o1 = tmem + K::T_O + ob * 128, o2 = o1 + 64;
+                if (n >= NB && !wait(&bars.o_free[ob], n / NB - 1)) break;
+                tc::tc_fence_after();
+                if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < A / 16; ++kk)
-                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, tc::sdesc(x + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
-                                       id_o1, kk > 0);
+                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, kk > 0);
                     if (BWD && split) {
 #pragma unroll
                         for (int kk = 0; kk < A / 16; ++kk)
-                            tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8, tc::sdesc(x + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024),
-                                           id_o1, 1u);
+                            tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, 1u);
                     }
                     tc::mma_commit(&bars.d1done);
-                    if (!wait(&bars.p_ready, n)) break;
-                    tc::tc_fence_after();
+                }
+                __syncwarp();
+                if (!wait(&bars.p_ready, n)) break;
+                tc::tc_fence_after();
+                if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_bf16(o2, tc::sdesc(z + kk * 2048, 8192, 1024), tc::sdesc(sb + K::OFF_P + kk * 32, 16, 1024),
-                                     id_o2, kk > 0);
+                    for (int kk = 0; kk < 4; ++kk) tc::mma_bf16(o2, dz + o + kk * 128, dp + kk * 2, id_o2, kk > 0);
                     tc::mma_commit(&bars.odone[ob]);
                 }
-                tc::mma_commit(&bars.free_s[n % NS]);
-                if (OUT && n + 1 < cnt) {
-                    if (!wait(&bars.full[(n + 1) % NS], (n + 1) / NS)) break;
-                    issue_p(n + 1);
-                }
+                __syncwarp();
             }
-            if (issued) {  // nothing of this CTA's is in flight when it exits (bounded)
-                tc::mma_commit(&bars.drain);
-                tc::mbar_wait(&bars.drain, 0, budget / 4);
+            if (leader) tc::mma_commit(&bars.free_s[st]);
+            __syncwarp();
+            if (++st == NS) {
+                st = 0;
+                ++ph;
             }
+            if (OUT && n + 1 < cnt) {
+                if (!wait(&bars.full[st], ph)) break;
+                issue_p(st);
+            }
+        }
+        if (issued) {  // nothing of this CTA's is in flight when it exits (bounded)
+            if (leader) tc::mma_commit(&bars.drain);
+            __syncwarp();
+            tc::mbar_wait(&bars.drain, 0, budget / 4);
         }
     } else if (warp == W_GATE) {
         double sum = 0.0;
@@ -300,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint4 *hi = reinterpret_cast<uint4 *>(base + K::OFF_W + (n & 1) * 2 * K::XB);
             uint4 *lo = hi + K::XB / 16;
             const float *kw = slots[n % SLOTS].kw;
-#pragma unroll
+#pragma unroll 2
             for (int i = gtid; i < K::XB / 16; i += 128) {  // 8 pieces of 16 bytes a row of a 64-column slab
                 const float f = kw[(i >> 3) & 63];
                 const uint4 u = y[i];
@@ -324,23 +372,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tc_fence_after();
             const Slot &sl = slots[n % SLOTS];
             const float2 cr = sl.c2[r < 0 ? 0 : r];
-#pragma unroll
-            for (int hb = 0; hb < 2; ++hb) {
-                float v[32];
-                tc::tmem_ld32(tmem + lane_base + K::T_P + hb * 32, v);
+#pragma unroll 1
+            for (int cb = 0; cb < 64; cb += 16) {
+                float v[16];
+                tc::tmem_ld16(tmem + lane_base + K::T_P + cb, v);
                 if (r >= 0) {
+                    const int d = rev ? cb - r : r - cb;  // column cb + j is on where d -+ j >= 0
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float4 cc = *reinterpret_cast<const float4 *>(&sl.c2[hb * 32 + j]);
-                        const int c0 = hb * 32 + j;
+                    for (int j = 0; j < 16; j += 2) {
+                        const float4 cc = *reinterpret_cast<const float4 *>(&sl.c2[cb + j]);
                         const float d0 = (cr.x - cc.x) + (cr.y - cc.y), d1 = (cr.x - cc.z) + (cr.y - cc.w);
-                        const bool on0 = rev ? c0 >= r : c0 <= r, on1 = rev ? c0 + 1 >= r : c0 + 1 <= r;
-                        v[j] = on0 ? v[j] * ex2(rev ? -d0 : d0) : 0.f;
-                        v[j + 1] = on1 ? v[j + 1] * ex2(rev ? -d1 : d1) : 0.f;
+                        const int o0 = rev ? d + j : d - j, o1 = rev ? d + j + 1 : d - j - 1;
+                        v[j] = o0 >= 0 ? v[j] * ex2(rev ? -d0 : d0) : 0.f;
+                        v[j + 1] = o1 >= 0 ? v[j + 1] * ex2(rev ? -d1 : d1) : 0.f;
                     }
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r, hb * 4 + c)) =
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r, (cb >> 3) + c)) =
                             make_uint4(tc::pack_bf16(v[8 * c], v[8 * c + 1]), tc::pack_bf16(v[8 * c + 2], v[8 * c + 3]),
                                        tc::pack_bf16(v[8 * c + 4], v[8 * c + 5]), tc::pack_bf16(v[8 * c + 6], v[8 * c + 7]));
                 }
@@ -356,6 +404,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (OUT) sin = nseg > 1 ? w.seg + ((size_t)bh * nseg + seg) * ab : (w.s0 ? w.s0 + bh * ab : nullptr);
         const bool st = nseg == 1 && w.s0_t;
         bool ok = true;
+        {  // the state that enters, as if a chunk had left it
+#pragma unroll 1
+            for (int cb = 0; cb < A; cb += 16) {
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[i] = sin && j >= 0 ? (st ? sin[(size_t)j * A + cb + i] : sin[(size_t)(cb + i) * B + j]) : 0.f;
+                tc::tmem_st16(tmem + lane_base + K::T_S + cb, v);
+            }
+        }
         for (int n = 0; ok && n < cnt; ++n) {
             ok = wait_gate(n) && (n == 0 || wait(&bars.d2done, n - 1));
             if (!ok) break;
@@ -365,34 +423,27 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) tc::mbar_arrive(&bars.gfree[(n - 1) % SLOTS]);
             }
             const float tot = slots[n % SLOTS].tot;
-#pragma unroll
-            for (int cb = 0; cb < A / 32; ++cb) {
+            if (OUT && n > 0) {  // the copy's last reader
+                ok = wait(&bars.d1done, n - 1);
+                if (!ok) break;
+                tc::tc_fence_after();
+            }
+#pragma unroll 1
+            for (int cb = 0; cb < A; cb += 32) {
                 float v[32];
-                if (n > 0) {
-                    tc::tmem_ld32(tmem + lane_base + K::T_S + cb * 32, v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = sin && j >= 0 ? (st ? sin[(size_t)j * A + cb * 32 + i] : sin[(size_t)(cb * 32 + i) * B + j]) : 0.f;
-                }
+                tc::tmem_ld32(tmem + lane_base + K::T_S + cb, v);
                 if (OUT) {
-                    if (cb == 0 && n > 0) {  // the copy's last reader
-                        ok = wait(&bars.d1done, n - 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                    }
                     uint32_t h[16], l[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
-                    tc::tmem_st16u(tmem + lane_base + K::T_H + cb * 16, h);
-                    if (BWD && split) tc::tmem_st16u(tmem + lane_base + K::T_L + cb * 16, l);
+                    tc::tmem_st16u(tmem + lane_base + K::T_H + cb / 2, h);
+                    if (BWD && split) tc::tmem_st16u(tmem + lane_base + K::T_L + cb / 2, l);
                 }
                 uint32_t u[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * tot);
-                tc::tmem_st32u(tmem + lane_base + K::T_S + cb * 32, u);
+                tc::tmem_st32u(tmem + lane_base + K::T_S + cb, u);
             }
-            if (!ok) break;
             warp_arrive(&bars.s_ready, lane);
         }
         float *sout = nullptr;
@@ -400,13 +451,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         else if (seg == nseg - 1 && w.s_end) sout = w.s_end + bh * ab;
         if (ok && sout && wait(&bars.d2done, cnt - 1)) {
             tc::tc_fence_after();
-#pragma unroll
-            for (int cb = 0; cb < A / 32; ++cb) {
-                float v[32];
-                tc::tmem_ld32(tmem + lane_base + K::T_S + cb * 32, v);
+#pragma unroll 1
+            for (int cb = 0; cb < A; cb += 16) {
+                float v[16];
+                tc::tmem_ld16(tmem + lane_base + K::T_S + cb, v);
                 if (j >= 0)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) sout[(size_t)(cb * 32 + i) * B + j] = v[i];
+                    for (int i = 0; i < 16; ++i) sout[(size_t)(cb + i) * B + j] = v[i];
             }
         }
     } else if (OUT && wg == 3) {
@@ -417,20 +468,21 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int n = 0; n < cnt; ++n) {
             const int t0 = chunk(n) * C, cl = min(C, L - t0), ob = n % NB;
             const size_t row0 = (size_t)bh * L + t0;
-            uint32_t xr[32];  // this lane's elements of the dots' other factor, two tokens a word
-            if (BWD && split) {
+            uint32_t xr[16];  // this lane's elements of the dots' other factor, half a chunk, two tokens a word
+            auto load_x = [&](int t) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const unsigned short *p = reinterpret_cast<const unsigned short *>(dx) + (row0 + 2 * i) * B + j;
-                    const uint32_t a = j >= 0 && 2 * i < cl ? p[0] : 0, b = j >= 0 && 2 * i + 1 < cl ? p[B] : 0;
+                for (int i = 0; i < 16; ++i) {
+                    const unsigned short *p = reinterpret_cast<const unsigned short *>(dx) + (row0 + t + 2 * i) * B + j;
+                    const uint32_t a = j >= 0 && t + 2 * i < cl ? p[0] : 0, b = j >= 0 && t + 2 * i + 1 < cl ? p[B] : 0;
                     xr[i] = a | (b << 16);
                 }
-            }
+            };
+            if (BWD && split) load_x(0);
             if (!wait_gate(n) || !wait(&bars.odone[ob], n / NB)) break;
             tc::tc_fence_after();
             const float *qw = slots[n % SLOTS].qw;
             const uint32_t o1 = tmem + lane_base + K::T_O + ob * 128;
-#pragma unroll
+#pragma unroll 1
             for (int hb = 0; hb < 2; ++hb) {
                 float v[32];
                 tc::tmem_ld32(o1 + hb * 32, v);
@@ -458,9 +510,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (BWD && split) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        v[2 * i] = j >= 0 ? v[2 * i] * bf_lo(xr[hb * 16 + i]) : 0.f;
-                        v[2 * i + 1] = j >= 0 ? v[2 * i + 1] * bf_hi(xr[hb * 16 + i]) : 0.f;
+                        v[2 * i] = j >= 0 ? v[2 * i] * bf_lo(xr[i]) : 0.f;
+                        v[2 * i + 1] = j >= 0 ? v[2 * i + 1] * bf_hi(xr[i]) : 0.f;
                     }
+                    if (hb == 0) load_x(32);
                     const float s = column_sums(v, lane);
                     if (hb * 32 + lane < cl) w.dot[((size_t)(warp & 3) * BH + bh) * L + t0 + hb * 32 + lane] = s;
                 }
