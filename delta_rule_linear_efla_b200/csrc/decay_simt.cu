@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(NT, 2)
         if (sin && i < a && j < nb) v = st ? sin[(size_t)(j0 + j) * a + i] : sin[(size_t)i * b + j0 + j];
         S[i * ZP + j] = v;
     }
-    double seg_sum = 0.0;
+    Sum seg_sum{0.f, 0.f};
 
     const int r4 = (tid >> 4) * 4, tc = tid & 15;  // P: rows r4.., columns tc + 16 j; out: columns 2 tc, 2 tc + 1
     for (int it = i0; it < i1; ++it) {
@@ -125,20 +125,19 @@ __global__ void __launch_bounds__(NT, 2)
         load_tile(Y, xp, static_cast<const T *>(w.y) + row0 * a, a, 0, ap, cl, tid);
         load_tile(Z, ZP, static_cast<const T *>(w.z) + row0 * b, b, j0, BT, cl, tid);
         if (warp == 0) {
-            const PairSum c = chunk_sums(g, bh, L, t0, lane);
-            const double cC = __shfl_sync(0xffffffffu, c.c1, 31);
-            const double cc[2] = {c.c0, c.c1};
+            const int t = t0 + 2 * lane;
+            const PairSum c = chunk_sums(gate_or_zero(g, bh, L, t), gate_or_zero(g, bh, L, t + 1), lane);
+            const Sum cC = last_sum(c), cc[2] = {c.c0, c.c1};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const float up = exp_sum(cc[e]), down = exp_sum(cC - cc[e]);
-                qw[t] = rev ? down : up;
-                kw[t] = rev ? up : down;
-                chi[t] = (float)cc[e];
-                clo[t] = (float)(cc[e] - (double)(float)cc[e]);
+                const float up = exp2_sum(cc[e]), down = exp2_sum(cC - cc[e]);
+                qw[2 * lane + e] = rev ? down : up;
+                kw[2 * lane + e] = rev ? up : down;
+                chi[2 * lane + e] = cc[e].hi;
+                clo[2 * lane + e] = cc[e].lo;
             }
-            if (lane == 0) tot[0] = exp_sum(cC);
-            seg_sum += cC;
+            if (lane == 0) tot[0] = exp2_sum(cC);
+            seg_sum = seg_sum + cC;
         }
         __syncthreads();
         if (OUT) {
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(NT, 2)
                     const int r = r4 + i, c = tc + 16 * j;
                     const float d = (chi[r] - chi[c]) + (clo[r] - clo[c]);
                     const bool on = rev ? c >= r : c <= r;
-                    P[r * PP + c] = on ? p[i][j] * expf(rev ? -d : d) : 0.f;
+                    P[r * PP + c] = on ? p[i][j] * exp2f(rev ? -d : d) : 0.f;
                 }
             __syncthreads();
             // ---- out = diag(q) X S + P Z: 4 rows x 2 columns a thread
@@ -271,7 +270,7 @@ __global__ void __launch_bounds__(NT, 2)
     }
     // every walk in the same direction finds the same decay of a segment: its first one writes it
     if (!OUT && warp == 0 && lane == 0 && blk == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
-        seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp_sum(seg_sum);
+        seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp2_sum(seg_sum);
 }
 
 template <typename T, typename TO>

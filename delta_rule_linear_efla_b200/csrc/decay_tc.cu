@@ -18,14 +18,18 @@
 //           a suffix sum of q.dq - k.dk that cancels down to the pairs that straddle a token; errors of
 //           D o P cancel with them (dq and dk round the same products), errors of two different state
 //           copies would not, and would grow with the square root of the sequence.
-// Decay factors and the sums over them are fp32 (their logarithms' sums fp64, decay_gate.cuh).
+// Decay factors and the sums over them are fp32 (their logarithms' sums two fp32 each, decay_gate.cuh).
 //
-// Warp roles (one CTA an SM, 19 warps):
+// Warp roles (one CTA an SM, 20 warps):
 //   0-3   weight:  Yw's halves from Y's tile
 //   4-7   mask:    D o P from TMEM into its operand tile
 //   8-11  state:   S^T after a chunk: its 16-bit copy, and scaled by the next chunk's e^{c_C}
 //   12-15 output:  out^T from TMEM to global memory, and its dots
-//   16    MMA issuer   17 TMA producer   18 decays (sums and weights, up to four chunks ahead)
+//   16    issues the state's products (S^T and O1^T)   17 those within the chunk (P and O2^T)
+//   18    TMA producer   19 decays (sums and weights, up to four chunks ahead)
+// The two issuers wait for different groups; one that waited for both ran the two loops one after the other.
+// Role bodies are loops of 16 to 32 columns: each is run once a chunk by one warp a scheduler, and unrolled
+// bodies were bound by instruction fetch (8 to 9 cycles an instruction against about 3).
 // Every mbarrier wait is bounded; a wait that gives up sets the device error word, lets what is in flight
 // land (again bounded), frees its tensor memory and exits.
 #include <cudaTypedefs.h>
@@ -42,8 +46,8 @@ static __device__ unsigned int g_decay_error = 0;
 
 namespace {
 
-constexpr int WARPS = 19, THREADS = WARPS * 32;
-constexpr int W_MMA = 16, W_TMA = 17, W_GATE = 18;
+constexpr int WARPS = 20, THREADS = WARPS * 32;
+constexpr int W_STATE = 16, W_INTRA = 17, W_TMA = 18, W_GATE = 19;
 constexpr int NS = 3;     // stages of X, Y, Z
 constexpr int SLOTS = 4;  // chunks of decay weights
 constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
@@ -60,18 +64,19 @@ struct Cfg {
     static constexpr int OFF_P = OFF_W + 4 * XB;    // D o P
     static constexpr int SMEM = OFF_P + 8192 + 1024;  // + alignment slack
     // tensor memory columns
-    static constexpr int NB = BWD && A == 128 ? 1 : 2;  // buffers of O1^T and O2^T
-    static constexpr uint32_t T_S = 0, T_H = A, T_L = T_H + A / 2, T_P = T_L + (BWD ? A / 2 : 0), T_O = T_P + 64;
-    static_assert(T_O + NB * 128 <= 512, "tensor memory");
+    static constexpr uint32_t T_S = 0, T_H = A, T_L = T_H + A / 2, T_P = T_L + (BWD ? A / 2 : 0), T_O1 = T_P + 128,
+                              T_O2 = T_O1 + 64;  // P twice
+    static_assert(T_O2 + 64 <= 512, "tensor memory");
 };
 
 struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
-    uint64_t full[NS], free_s[NS], gready[SLOTS], y_free[2], pdone, d1done, d2done, odone[2], drain;
+    uint64_t full[NS], gready[SLOTS], y_free[2], pdone[2], d1done, d2done, o2done, drain[2];
     // one arrival from each of four warps
-    uint64_t gfree[SLOTS], y_ready[2], p_ready, s_ready, o_free[2];
+    uint64_t gfree[SLOTS], y_ready[2], p_ready, s_ready, o_free;
+    uint64_t free_s[NS];  // one from each issuer
 };
-constexpr int BARS_ONE = 2 * NS + SLOTS + 2 + 3 + 2 + 1;
+constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + SLOTS + 2 + 2 + 3 + 2;
 
 struct Slot {
     float qw[C], kw[C];
@@ -114,6 +119,55 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
             *abort_flag = 1;
             return false;
         }
+    }
+}
+
+// 16 lanes x 32 columns of tensor memory, a row of eight columns on four threads: v[4 k + 2 e + i] is row
+// lane / 4 + 8 e, column 8 k + 2 (lane % 4) + i.  Waits for completion.
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 32 lanes x 16 columns of raw words into tensor memory, without the wait for completion.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+// 32 lanes x 32 columns from each of two places in tensor memory, one wait.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t tb, float (&a)[32], float (&b)[32]) {
+    uint32_t r[64];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+        "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
+          "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]),
+          "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
+          "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(ta), "r"(tb)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        a[i] = __uint_as_float(r[i]);
+        b[i] = __uint_as_float(r[32 + i]);
     }
 }
 
@@ -163,7 +217,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     walk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Walks ws, const Gate g, int BH, int L,
                    int nseg, int seg_chunks, float *__restrict__ seg_e) {
     using K = Cfg<A, B, BWD>;
-    constexpr int NB = K::NB;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = tc::smem_u32(smem_raw);
     uint8_t *base = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
@@ -185,7 +238,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (tid == 0) {
         uint64_t *b = reinterpret_cast<uint64_t *>(&bars);
-        for (int i = 0; i < (int)(sizeof(Bars) / sizeof(uint64_t)); ++i) tc::mbar_init(b + i, i < BARS_ONE ? 1 : 4);
+        for (int i = 0; i < BARS; ++i) tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS - NS ? 4 : OUT ? 2 : 1);
         tc::fence_mbar_init();
         abort_flag = 0;
         tc::tma_prefetch_desc(&maps.x[wi]);
@@ -223,46 +276,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (abort_flag)  // let this CTA's own copies land before it exits (bounded)
                 for (int m = n > NS ? n - NS : 0; m < n; ++m) tc::mbar_wait(&bars.full[m % NS], (m / NS) & 1, budget / 8);
         }
-    } else if (warp == W_MMA) {
+    } else if (warp == W_STATE) {
         // The whole warp runs the loop and one elected lane issues, so that descriptors are warp-uniform.
-        constexpr uint32_t id_p = tc::idesc_bf16(64, 64, false, false);
-        constexpr uint32_t id_o1 = tc::idesc_bf16(B, 64, false, false);
-        constexpr uint32_t id_o2 = tc::idesc_bf16(B, 64, true, false);
-        constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true);
-        // descriptors of the first stage / buffer; others are their distance / 16 further on
-        const uint64_t dx = tc::sdesc(sb + K::OFF_X, 16, 1024), dy = tc::sdesc(sb + K::OFF_Y, 16, 1024);
-        const uint64_t dz = tc::sdesc(sb + K::OFF_Z, 8192, 1024), dw = tc::sdesc(sb + K::OFF_W, 8192, 1024);
-        const uint64_t dp = tc::sdesc(sb + K::OFF_P, 16, 1024);
+        constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true), id_o1 = tc::idesc_bf16(B, 64, false, false);
+        const uint64_t dx = tc::sdesc(sb + K::OFF_X, 16, 1024), dz = tc::sdesc(sb + K::OFF_Z, 8192, 1024);
+        const uint64_t dw = tc::sdesc(sb + K::OFF_W, 8192, 1024);
         const bool leader = elect();
-        auto issue_p = [&](int st) {
-            if (leader) {
-                const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-#pragma unroll
-                for (int kk = 0; kk < A / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
-                    tc::mma_bf16(tmem + K::T_P, dx + o + off, dy + o + off, id_p, kk > 0);
-                }
-                tc::mma_commit(&bars.pdone);
-            }
-            __syncwarp();
-        };
-        bool issued = false, ok = true;
-        if (OUT) {
-            ok = wait(&bars.full[0], 0);
-            if (ok) {
-                issued = true;
-                issue_p(0);
-            }
-        }
         int st = 0, ph = 0;  // stage and its pass
-        for (int n = 0; ok && n < cnt; ++n) {
+        for (int n = 0; n < cnt; ++n) {
             const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-            // S^T += Z^T Yw
-            if (!OUT && !wait(&bars.full[st], ph)) break;
-            if (!wait(&bars.y_ready[n & 1], n >> 1) || !wait(&bars.s_ready, n)) break;
+            if (!wait(&bars.full[st], ph) || !wait(&bars.y_ready[n & 1], n >> 1) || !wait(&bars.s_ready, n)) break;
             tc::tc_fence_after();
-            issued = true;
-            if (leader) {
+            if (leader) {  // S^T += Z^T Yw
                 const uint64_t yw = dw + (uint64_t)((n & 1) * (2 * K::XB >> 4));
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -274,30 +299,21 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
             if (OUT) {
-                const int ob = n % NB;
-                const uint32_t o1 = tmem + K::T_O + ob * 128, o2 = o1 + 64;
-                if (n >= NB && !wait(&bars.o_free[ob], n / NB - 1)) break;
+                if (n > 0 && !wait(&bars.o_free, n - 1)) break;
                 tc::tc_fence_after();
-                if (leader) {
+                if (leader) {  // O1^T = S^T X^T
 #pragma unroll
                     for (int kk = 0; kk < A / 16; ++kk)
-                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, kk > 0);
+                        tc::mma_tmem_a(tmem + K::T_O1, tmem + K::T_H + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                                       id_o1, kk > 0);
                     if (BWD && split) {
 #pragma unroll
                         for (int kk = 0; kk < A / 16; ++kk)
-                            tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, 1u);
+                            tc::mma_tmem_a(tmem + K::T_O1, tmem + K::T_L + kk * 8,
+                                           dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, 1u);
                     }
                     tc::mma_commit(&bars.d1done);
                 }
-                __syncwarp();
-                if (!wait(&bars.p_ready, n)) break;
-                tc::tc_fence_after();
-                if (leader) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) tc::mma_bf16(o2, dz + o + kk * 128, dp + kk * 2, id_o2, kk > 0);
-                    tc::mma_commit(&bars.odone[ob]);
-                }
-                __syncwarp();
             }
             if (leader) tc::mma_commit(&bars.free_s[st]);
             __syncwarp();
@@ -305,40 +321,83 @@ __global__ void __launch_bounds__(THREADS, 1)
                 st = 0;
                 ++ph;
             }
-            if (OUT && n + 1 < cnt) {
-                if (!wait(&bars.full[st], ph)) break;
-                issue_p(st);
+        }
+        // nothing of this CTA's is in flight when it exits (bounded)
+        if (leader) tc::mma_commit(&bars.drain[0]);
+        __syncwarp();
+        tc::mbar_wait(&bars.drain[0], 0, budget / 4);
+    } else if (OUT && warp == W_INTRA) {
+        constexpr uint32_t id_p = tc::idesc_bf16(64, 64, false, false), id_o2 = tc::idesc_bf16(B, 64, true, false);
+        const uint64_t dx = tc::sdesc(sb + K::OFF_X, 16, 1024), dy = tc::sdesc(sb + K::OFF_Y, 16, 1024);
+        const uint64_t dz = tc::sdesc(sb + K::OFF_Z, 8192, 1024), dp = tc::sdesc(sb + K::OFF_P, 16, 1024);
+        const bool leader = elect();
+        auto issue_p = [&](int n, int st) {  // P = X Y^T
+            if (leader) {
+                const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
+#pragma unroll
+                for (int kk = 0; kk < A / 16; ++kk) {
+                    const uint32_t off = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
+                    tc::mma_bf16(tmem + K::T_P + (n & 1) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
+                }
+                tc::mma_commit(&bars.pdone[n & 1]);
             }
-        }
-        if (issued) {  // nothing of this CTA's is in flight when it exits (bounded)
-            if (leader) tc::mma_commit(&bars.drain);
             __syncwarp();
-            tc::mbar_wait(&bars.drain, 0, budget / 4);
-        }
-    } else if (warp == W_GATE) {
-        double sum = 0.0;
+        };
+        if (wait(&bars.full[0], 0)) issue_p(0, 0);
+        int st = 0, ph = 0;
         for (int n = 0; n < cnt; ++n) {
-            const PairSum c = chunk_sums(g, bh, L, chunk(n) * C, lane);
-            const double cC = __shfl_sync(0xffffffffu, c.c1, 31), cc[2] = {c.c0, c.c1};
-            sum += cC;
+            const int cur = st;
+            if (++st == NS) {
+                st = 0;
+                ++ph;
+            }
+            if (n + 1 < cnt) {
+                if (!wait(&bars.full[st], ph)) break;
+                issue_p(n + 1, st);
+            }
+            if (!wait(&bars.p_ready, n) || (n > 0 && !wait(&bars.o_free, n - 1))) break;
+            tc::tc_fence_after();
+            if (leader) {  // O2^T = Z^T (D o P)^T
+                const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) tc::mma_bf16(tmem + K::T_O2, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
+                tc::mma_commit(&bars.o2done);
+                tc::mma_commit(&bars.free_s[cur]);
+            }
+            __syncwarp();
+        }
+        if (leader) tc::mma_commit(&bars.drain[1]);
+        __syncwarp();
+        tc::mbar_wait(&bars.drain[1], 0, budget / 4);
+    } else if (warp == W_GATE) {
+        Sum sum{0.f, 0.f};
+        int t = chunk(0) * C + 2 * lane;
+        float l0 = gate_or_zero(g, bh, L, t), l1 = gate_or_zero(g, bh, L, t + 1);
+        for (int n = 0; n < cnt; ++n) {
+            const PairSum c = chunk_sums(l0, l1, lane);
+            const Sum cC = last_sum(c), cc[2] = {c.c0, c.c1};
+            sum = sum + cC;
+            if (n + 1 < cnt) {  // the next chunk's, while this one's weights are made
+                t = chunk(n + 1) * C + 2 * lane;
+                l0 = gate_or_zero(g, bh, L, t);
+                l1 = gate_or_zero(g, bh, L, t + 1);
+            }
             if (n >= SLOTS && !wait(&bars.gfree[n % SLOTS], n / SLOTS - 1)) break;
             Slot &sl = slots[n % SLOTS];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = 2 * lane + e;
-                const float up = exp_sum(cc[e]), down = exp_sum(cC - cc[e]);
-                sl.qw[t] = rev ? down : up;
-                sl.kw[t] = rev ? up : down;
-                const double c2 = cc[e] * 1.4426950408889634;
-                sl.c2[t] = make_float2((float)c2, (float)(c2 - (double)(float)c2));
+                const float up = exp2_sum(cc[e]), down = exp2_sum(cC - cc[e]);
+                sl.qw[2 * lane + e] = rev ? down : up;
+                sl.kw[2 * lane + e] = rev ? up : down;
+                sl.c2[2 * lane + e] = make_float2(cc[e].hi, cc[e].lo);
             }
-            if (lane == 0) sl.tot = exp_sum(cC);
+            if (lane == 0) sl.tot = exp2_sum(cC);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars.gready[n % SLOTS]);
         }
         // every walk in the same direction finds the same decay of a segment: its first one writes it
         if (!OUT && lane == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
-            seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp_sum(sum);
+            seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp2_sum(sum);
     } else if (wg == 0) {
         // ---------------------------------------------------------- Yw
         for (int n = 0; n < cnt; ++n) {
@@ -365,34 +424,49 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (wg == 1) {
         // ---------------------------------------------------------- D o P
-        const int r = acc_row<64>(warp & 3, lane);
+        // a thread holds rows r and r + 8 of its warp's 16, two columns of every eight
+        const int r = 16 * warp - 64 + (lane >> 2), cq = 2 * (lane & 3);
         uint8_t *pt = base + K::OFF_P;
         for (int n = 0; OUT && n < cnt; ++n) {
-            if (!wait_gate(n) || !wait(&bars.pdone, n)) break;
+            if (!wait_gate(n) || !wait(&bars.pdone[n & 1], n >> 1)) break;
             tc::tc_fence_after();
             const Slot &sl = slots[n % SLOTS];
-            const float2 cr = sl.c2[r < 0 ? 0 : r];
+            const float2 ca = sl.c2[r], cb = sl.c2[r + 8];
+            bool ok = true;
 #pragma unroll 1
-            for (int cb = 0; cb < 64; cb += 16) {
+            for (int h = 0; h < 64; h += 32) {
                 float v[16];
-                tc::tmem_ld16(tmem + lane_base + K::T_P + cb, v);
-                if (r >= 0) {
-                    const int d = rev ? cb - r : r - cb;  // column cb + j is on where d -+ j >= 0
+                tmem_ld_16x256(tmem + lane_base + K::T_P + (n & 1) * 64 + h, v);
+                uint32_t u[8];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        const float4 cc = *reinterpret_cast<const float4 *>(&sl.c2[cb + j]);
-                        const float d0 = (cr.x - cc.x) + (cr.y - cc.y), d1 = (cr.x - cc.z) + (cr.y - cc.w);
-                        const int o0 = rev ? d + j : d - j, o1 = rev ? d + j + 1 : d - j - 1;
-                        v[j] = o0 >= 0 ? v[j] * ex2(rev ? -d0 : d0) : 0.f;
-                        v[j + 1] = o1 >= 0 ? v[j + 1] * ex2(rev ? -d1 : d1) : 0.f;
+                for (int k = 0; k < 4; ++k) {
+                    const int c = h + 8 * k + cq;
+                    const float4 cc = *reinterpret_cast<const float4 *>(&sl.c2[c]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {  // row r + 8 e, columns c and c + 1
+                        const float2 cr = e ? cb : ca;
+                        float d0 = (cr.x - cc.x) + (cr.y - cc.y), d1 = (cr.x - cc.z) + (cr.y - cc.w);
+                        int a0 = r + 8 * e - c;  // column c is on where a0 >= 0 (forwards) or <= 0
+                        int a1 = a0 - 1;
+                        if (rev) {
+                            d0 = -d0; d1 = -d1;
+                            a0 = -a0; a1 = -a1;
+                        }
+                        u[2 * k + e] = tc::pack_bf16(a0 >= 0 ? v[4 * k + 2 * e] * ex2(d0) : 0.f,
+                                                     a1 >= 0 ? v[4 * k + 2 * e + 1] * ex2(d1) : 0.f);
                     }
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r, (cb >> 3) + c)) =
-                            make_uint4(tc::pack_bf16(v[8 * c], v[8 * c + 1]), tc::pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                                       tc::pack_bf16(v[8 * c + 4], v[8 * c + 5]), tc::pack_bf16(v[8 * c + 6], v[8 * c + 7]));
                 }
+                if (h == 0 && n > 0) {  // the tile's last reader
+                    ok = wait(&bars.o2done, n - 1);
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint32_t *>(pt + tc::sw128_off(r + 8 * e, (h >> 3) + k) + 2 * cq) = u[2 * k + e];
             }
+            if (!ok) break;
             tc::fence_async_smem();
             warp_arrive(&bars.p_ready, lane);
         }
@@ -436,14 +510,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                     uint32_t h[16], l[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
-                    tc::tmem_st16u(tmem + lane_base + K::T_H + cb / 2, h);
-                    if (BWD && split) tc::tmem_st16u(tmem + lane_base + K::T_L + cb / 2, l);
+                    tmem_st16(tmem + lane_base + K::T_H + cb / 2, h);
+                    if (BWD && split) tmem_st16(tmem + lane_base + K::T_L + cb / 2, l);
                 }
-                uint32_t u[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(v[i] * tot);
-                tc::tmem_st32u(tmem + lane_base + K::T_S + cb, u);
+                for (int e = 0; e < 32; e += 16) {
+                    uint32_t u[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[e + i] * tot);
+                    tmem_st16(tmem + lane_base + K::T_S + cb + e, u);
+                }
             }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             warp_arrive(&bars.s_ready, lane);
         }
         float *sout = nullptr;
@@ -466,7 +544,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         TO *out = static_cast<TO *>(w.out);
         const __nv_bfloat16 *dx = static_cast<const __nv_bfloat16 *>(w.dotx);
         for (int n = 0; n < cnt; ++n) {
-            const int t0 = chunk(n) * C, cl = min(C, L - t0), ob = n % NB;
+            const int t0 = chunk(n) * C, cl = min(C, L - t0);
             const size_t row0 = (size_t)bh * L + t0;
             uint32_t xr[16];  // this lane's elements of the dots' other factor, half a chunk, two tokens a word
             auto load_x = [&](int t) {
@@ -478,28 +556,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             };
             if (BWD && split) load_x(0);
-            if (!wait_gate(n) || !wait(&bars.odone[ob], n / NB)) break;
+            if (!wait_gate(n) || !wait(&bars.d1done, n) || !wait(&bars.o2done, n)) break;
             tc::tc_fence_after();
             const float *qw = slots[n % SLOTS].qw;
-            const uint32_t o1 = tmem + lane_base + K::T_O + ob * 128;
+            const uint32_t o1 = tmem + lane_base + K::T_O1;
 #pragma unroll 1
             for (int hb = 0; hb < 2; ++hb) {
-                float v[32];
-                tc::tmem_ld32(o1 + hb * 32, v);
+                float v[32], u[32];
+                tmem_ld32x2(o1 + hb * 32, o1 + 64 + hb * 32, v, u);
+                if (hb == 1) warp_arrive(&bars.o_free, lane);
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(qw + hb * 32 + i);
-                    v[i] *= f.x; v[i + 1] *= f.y; v[i + 2] *= f.z; v[i + 3] *= f.w;
-                }
-#pragma unroll
-                for (int qb = 0; qb < 2; ++qb) {
-                    float u[16];
-                    tc::tmem_ld16(o1 + 64 + hb * 32 + qb * 16, u);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[qb * 16 + i] += u[i];
+                    v[i] = fmaf(f.x, v[i], u[i]); v[i + 1] = fmaf(f.y, v[i + 1], u[i + 1]);
+                    v[i + 2] = fmaf(f.z, v[i + 2], u[i + 2]); v[i + 3] = fmaf(f.w, v[i + 3], u[i + 3]);
                 }
                 if (hb == 1) {
-                    warp_arrive(&bars.o_free[ob], lane);
+                    __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
                 }
                 if (j >= 0) {
