@@ -20,13 +20,13 @@
 //           copies would not, and would grow with the square root of the sequence.
 // Decay factors and the sums over them are fp32 (their logarithms' sums two fp32 each, decay_gate.cuh).
 //
-// Warp roles (one CTA an SM, 20 warps):
+// Warp roles (one CTA an SM, 24 warps):
 //   0-3   weight:  Yw's halves from Y's tile
 //   4-7   mask:    D o P from TMEM into its operand tile
 //   8-11  state:   S^T after a chunk: its 16-bit copy, and scaled by the next chunk's e^{c_C}
-//   12-15 output:  out^T from TMEM to global memory, and its dots
-//   16    issues the state's products (S^T and O1^T)   17 those within the chunk (P and O2^T)
-//   18    TMA producer   19 decays (sums and weights, up to four chunks ahead)
+//   12-19 output:  out^T from TMEM to global memory, and its dots; half a chunk's tokens each four warps
+//   20    issues the state's products (S^T and O1^T)   21 those within the chunk (P and O2^T)
+//   22    TMA producer   23 decays (sums and weights, up to four chunks ahead)
 // The two issuers wait for different groups; one that waited for both ran the two loops one after the other.
 // Role bodies are loops of 16 to 32 columns: each is run once a chunk by one warp a scheduler, and unrolled
 // bodies were bound by instruction fetch (8 to 9 cycles an instruction against about 3).
@@ -46,8 +46,8 @@ static __device__ unsigned int g_decay_error = 0;
 
 namespace {
 
-constexpr int WARPS = 20, THREADS = WARPS * 32;
-constexpr int W_STATE = 16, W_INTRA = 17, W_TMA = 18, W_GATE = 19;
+constexpr int WARPS = 24, THREADS = WARPS * 32;
+constexpr int W_STATE = 20, W_INTRA = 21, W_TMA = 22, W_GATE = 23;
 constexpr int NS = 3;     // stages of X, Y, Z
 constexpr int SLOTS = 4;  // chunks of decay weights
 constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
@@ -64,19 +64,23 @@ struct Cfg {
     static constexpr int OFF_P = OFF_W + 4 * XB;    // D o P
     static constexpr int SMEM = OFF_P + 8192 + 1024;  // + alignment slack
     // tensor memory columns
-    static constexpr uint32_t T_S = 0, T_H = A, T_L = T_H + A / 2, T_P = T_L + (BWD ? A / 2 : 0), T_O1 = T_P + 128,
-                              T_O2 = T_O1 + 64;  // P twice
-    static_assert(T_O2 + 64 <= 512, "tensor memory");
+    // buffers of P, and of O1^T and O2^T: a second one of the outputs first (their loop, from free through
+    // two products to done and read, is the longer one)
+    static constexpr int NO = BWD && A == 128 ? 1 : 2, NP = A == 128 && !BWD ? 1 : 2;
+    static constexpr uint32_t T_S = 0, T_H = A, T_L = T_H + A / 2, T_P = T_L + (BWD ? A / 2 : 0), T_O = T_P + NP * 64;
+    static_assert(T_O + NO * 128 <= 512, "tensor memory");
 };
 
 struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
-    uint64_t full[NS], gready[SLOTS], y_free[2], pdone[2], d1done, d2done, o2done, drain[2];
+    uint64_t full[NS], gready[SLOTS], y_free[2], pdone[2], d1done, d2done, o1done[2], o2done, o2done_b[2], drain[2];
     // one arrival from each of four warps
-    uint64_t gfree[SLOTS], y_ready[2], p_ready, s_ready, o_free;
-    uint64_t free_s[NS];  // one from each issuer
+    uint64_t y_ready[2], p_ready, s_ready;
+    uint64_t gfree[SLOTS], o_free[2];  // eight warps with output, four without
+    uint64_t free_s[NS];               // one from each issuer
 };
-constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + SLOTS + 2 + 2 + 3 + 2;
+constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + SLOTS + 2 + 2 + 2 + 2 + 1 + 2 + 2, BARS_FOUR = BARS_ONE + 4,
+              BARS_OUT = BARS_FOUR + SLOTS + 2;
 
 struct Slot {
     float qw[C], kw[C];
@@ -146,28 +150,23 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-// 32 lanes x 32 columns from each of two places in tensor memory, one wait.
-__device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t tb, float (&a)[32], float (&b)[32]) {
-    uint32_t r[64];
+// 32 lanes x 16 columns from each of two places in tensor memory, one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
+    uint32_t r[32];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-        "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
           "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]),
-          "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]),
-          "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]),
-          "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(ta), "r"(tb)
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 16; ++i) {
         a[i] = __uint_as_float(r[i]);
-        b[i] = __uint_as_float(r[32 + i]);
+        b[i] = __uint_as_float(r[16 + i]);
     }
 }
 
@@ -238,7 +237,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     if (tid == 0) {
         uint64_t *b = reinterpret_cast<uint64_t *>(&bars);
-        for (int i = 0; i < BARS; ++i) tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS - NS ? 4 : OUT ? 2 : 1);
+        for (int i = 0; i < BARS; ++i) 
+            tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS_FOUR ? 4 : i < BARS_OUT ? (OUT ? 8 : 4) : (OUT ? 2 : 1));
         tc::fence_mbar_init();
         abort_flag = 0;
         tc::tma_prefetch_desc(&maps.x[wi]);
@@ -299,20 +299,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
             if (OUT) {
-                if (n > 0 && !wait(&bars.o_free, n - 1)) break;
+                const int ob = n % K::NO;
+                if (n >= K::NO && !wait(&bars.o_free[ob], n / K::NO - 1)) break;
                 tc::tc_fence_after();
                 if (leader) {  // O1^T = S^T X^T
+                    const uint32_t o1 = tmem + K::T_O + ob * 128;
 #pragma unroll
                     for (int kk = 0; kk < A / 16; ++kk)
-                        tc::mma_tmem_a(tmem + K::T_O1, tmem + K::T_H + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
+                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
                                        id_o1, kk > 0);
                     if (BWD && split) {
 #pragma unroll
                         for (int kk = 0; kk < A / 16; ++kk)
-                            tc::mma_tmem_a(tmem + K::T_O1, tmem + K::T_L + kk * 8,
+                            tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8,
                                            dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, 1u);
                     }
                     tc::mma_commit(&bars.d1done);
+                    tc::mma_commit(&bars.o1done[ob]);
                 }
             }
             if (leader) tc::mma_commit(&bars.free_s[st]);
@@ -337,9 +340,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int kk = 0; kk < A / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
-                    tc::mma_bf16(tmem + K::T_P + (n & 1) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
+                    tc::mma_bf16(tmem + K::T_P + (n % K::NP) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
                 }
-                tc::mma_commit(&bars.pdone[n & 1]);
+                tc::mma_commit(&bars.pdone[n % K::NP]);
             }
             __syncwarp();
         };
@@ -351,17 +354,23 @@ __global__ void __launch_bounds__(THREADS, 1)
                 st = 0;
                 ++ph;
             }
+            // P of the next chunk: with one buffer once the mask has read this one's
+            if (K::NP == 1 && !wait(&bars.p_ready, n)) break;
             if (n + 1 < cnt) {
                 if (!wait(&bars.full[st], ph)) break;
+                tc::tc_fence_after();
                 issue_p(n + 1, st);
             }
-            if (!wait(&bars.p_ready, n) || (n > 0 && !wait(&bars.o_free, n - 1))) break;
+            const int ob = n % K::NO;
+            if ((K::NP == 2 && !wait(&bars.p_ready, n)) || (n >= K::NO && !wait(&bars.o_free[ob], n / K::NO - 1))) break;
             tc::tc_fence_after();
             if (leader) {  // O2^T = Z^T (D o P)^T
                 const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) tc::mma_bf16(tmem + K::T_O2, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
+                for (int kk = 0; kk < 4; ++kk)
+                    tc::mma_bf16(tmem + K::T_O + ob * 128 + 64, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
                 tc::mma_commit(&bars.o2done);
+                tc::mma_commit(&bars.o2done_b[ob]);
                 tc::mma_commit(&bars.free_s[cur]);
             }
             __syncwarp();
@@ -428,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int r = 16 * warp - 64 + (lane >> 2), cq = 2 * (lane & 3);
         uint8_t *pt = base + K::OFF_P;
         for (int n = 0; OUT && n < cnt; ++n) {
-            if (!wait_gate(n) || !wait(&bars.pdone[n & 1], n >> 1)) break;
+            if (!wait_gate(n) || !wait(&bars.pdone[n % K::NP], n / K::NP)) break;
             tc::tc_fence_after();
             const Slot &sl = slots[n % SLOTS];
             const float2 ca = sl.c2[r], cb = sl.c2[r + 8];
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll 1
             for (int h = 0; h < 64; h += 32) {
                 float v[16];
-                tmem_ld_16x256(tmem + lane_base + K::T_P + (n & 1) * 64 + h, v);
+                tmem_ld_16x256(tmem + lane_base + K::T_P + (n % K::NP) * 64 + h, v);
                 uint32_t u[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -538,58 +547,54 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < 16; ++i) sout[(size_t)(cb + i) * B + j] = v[i];
             }
         }
-    } else if (OUT && wg == 3) {
+    } else if (OUT && (wg == 3 || wg == 4)) {
         // ---------------------------------------------------------- out
-        const int j = acc_row<B>(warp & 3, lane);
-        TO *out = static_cast<TO *>(w.out);
-        const __nv_bfloat16 *dx = static_cast<const __nv_bfloat16 *>(w.dotx);
+        const int j = acc_row<B>(warp & 3, lane), h0 = wg == 3 ? 0 : 32;  // tokens h0 .. h0 + 31 of a chunk
         for (int n = 0; n < cnt; ++n) {
-            const int t0 = chunk(n) * C, cl = min(C, L - t0);
+            const int t0 = chunk(n) * C + h0, cl = min(32, L - t0), ob = n % K::NO;
             const size_t row0 = (size_t)bh * L + t0;
-            uint32_t xr[16];  // this lane's elements of the dots' other factor, half a chunk, two tokens a word
-            auto load_x = [&](int t) {
+            uint32_t xr[16];  // this lane's elements of the dots' other factor, two tokens a word
+            if (BWD && split) {
+                const unsigned short *dx = static_cast<const unsigned short *>(w.dotx) + row0 * B + j;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const unsigned short *p = reinterpret_cast<const unsigned short *>(dx) + (row0 + t + 2 * i) * B + j;
-                    const uint32_t a = j >= 0 && t + 2 * i < cl ? p[0] : 0, b = j >= 0 && t + 2 * i + 1 < cl ? p[B] : 0;
+                    const uint32_t a = j >= 0 && 2 * i < cl ? dx[2 * i * B] : 0, b = j >= 0 && 2 * i + 1 < cl ? dx[(2 * i + 1) * B] : 0;
                     xr[i] = a | (b << 16);
                 }
-            };
-            if (BWD && split) load_x(0);
-            if (!wait_gate(n) || !wait(&bars.d1done, n) || !wait(&bars.o2done, n)) break;
+            }
+            if (!wait_gate(n) || !wait(&bars.o1done[ob], n / K::NO) || !wait(&bars.o2done_b[ob], n / K::NO)) break;
             tc::tc_fence_after();
-            const float *qw = slots[n % SLOTS].qw;
-            const uint32_t o1 = tmem + lane_base + K::T_O1;
-#pragma unroll 1
-            for (int hb = 0; hb < 2; ++hb) {
-                float v[32], u[32];
-                tmem_ld32x2(o1 + hb * 32, o1 + 64 + hb * 32, v, u);
-                if (hb == 1) warp_arrive(&bars.o_free, lane);
+            const float *qw = slots[n % SLOTS].qw + h0;
+            const uint32_t o1 = tmem + lane_base + K::T_O + ob * 128 + h0;
+            float v[32];
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(qw + hb * 32 + i);
-                    v[i] = fmaf(f.x, v[i], u[i]); v[i + 1] = fmaf(f.y, v[i + 1], u[i + 1]);
-                    v[i + 2] = fmaf(f.z, v[i + 2], u[i + 2]); v[i + 3] = fmaf(f.w, v[i + 3], u[i + 3]);
-                }
-                if (hb == 1) {
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
-                }
-                if (j >= 0) {
+            for (int e = 0; e < 32; e += 16) {
+                float a[16], b[16];
+                tmem_ld16x2(o1 + e, o1 + 64 + e, a, b);
+                if (e == 16) warp_arrive(&bars.o_free[ob], lane);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (hb * 32 + i < cl) put(out + (row0 + hb * 32 + i) * B + j, v[i]);
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(qw + e + i);
+                    v[e + i] = fmaf(f.x, a[i], b[i]); v[e + i + 1] = fmaf(f.y, a[i + 1], b[i + 1]);
+                    v[e + i + 2] = fmaf(f.z, a[i + 2], b[i + 2]); v[e + i + 3] = fmaf(f.w, a[i + 3], b[i + 3]);
                 }
-                if (BWD && split) {
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
+            if (j >= 0) {
+                TO *out = static_cast<TO *>(w.out) + row0 * B + j;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        v[2 * i] = j >= 0 ? v[2 * i] * bf_lo(xr[i]) : 0.f;
-                        v[2 * i + 1] = j >= 0 ? v[2 * i + 1] * bf_hi(xr[i]) : 0.f;
-                    }
-                    if (hb == 0) load_x(32);
-                    const float s = column_sums(v, lane);
-                    if (hb * 32 + lane < cl) w.dot[((size_t)(warp & 3) * BH + bh) * L + t0 + hb * 32 + lane] = s;
+                for (int i = 0; i < 32; ++i)
+                    if (i < cl) put(out + i * B, v[i]);
+            }
+            if (BWD && split) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[2 * i] = j >= 0 ? v[2 * i] * bf_lo(xr[i]) : 0.f;
+                    v[2 * i + 1] = j >= 0 ? v[2 * i + 1] * bf_hi(xr[i]) : 0.f;
                 }
+                const float s = column_sums(v, lane);
+                if (lane < cl) w.dot[((size_t)(warp & 3) * BH + bh) * L + t0 + lane] = s;
             }
         }
     }
