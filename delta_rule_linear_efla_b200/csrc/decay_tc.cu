@@ -84,7 +84,8 @@ constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + SLOTS + 2 + 2 + 2 + 2 + 1
 
 struct Slot {
     float qw[C], kw[C];
-    float2 c2[C];  // running sum in units of log 2, hi and lo
+    float gw[C];   // 2^(c_end - c) within a token's group of eight (end: its last token in walking order)
+    float2 c2[C];  // running sum in units of log 2 (its negative backwards), hi and lo
     float tot, pad[3];
 };
 
@@ -126,20 +127,18 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
     }
 }
 
-// 16 lanes x 32 columns of tensor memory, a row of eight columns on four threads: v[4 k + 2 e + i] is row
+// 16 lanes x 16 columns of tensor memory, a row of eight columns on four threads: v[4 k + 2 e + i] is row
 // lane / 4 + 8 e, column 8 k + 2 (lane % 4) + i.  Waits for completion.
-__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
         : "r"(taddr)
         : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 32 lanes x 16 columns of raw words into tensor memory, without the wait for completion.
@@ -186,10 +185,39 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
+// Two fp32 in a 64-bit register: the packed arithmetic of sm_100 does both in one instruction.
+struct F2 {
+    uint64_t r;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 a;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a.r) : "f"(x), "f"(y));
+    return a;
+}
+__device__ __forceinline__ float2 unpack(F2 a) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(a.r));
+    return v;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    F2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.r) : "l"(a.r), "l"(b.r));
+    return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.r) : "l"(a.r), "l"(b.r), "l"(c.r));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack(F2 a) {
+    const float2 v = unpack(a);
+    return tc::pack_bf16(v.x, v.y);
+}
+
 // Two floats as packed bf16 halves: x = hi + lo to 2^-17 of |x|.
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
-    hi = tc::pack_bf16(x, y);
-    lo = tc::pack_bf16(x - bf_lo(hi), y - bf_hi(hi));
+__device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
+    hi = pack(x);
+    lo = pack(fma2(f2(bf_lo(hi), bf_hi(hi)), f2(-1.f, -1.f), x));
 }
 
 // The sums over a warp's lanes of 32 columns: lane l ends with column l's.
@@ -208,6 +236,12 @@ __device__ __forceinline__ float column_sums(float (&p)[32], int lane) {
 
 __device__ __forceinline__ void put(float *p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put2(float *p, float *q, float x, float y) { *p = x; *q = y; }
+__device__ __forceinline__ void put2(__nv_bfloat16 *p, __nv_bfloat16 *q, float x, float y) {
+    const uint32_t u = tc::pack_bf16(x, y);
+    *reinterpret_cast<unsigned short *>(p) = (unsigned short)u;
+    *reinterpret_cast<unsigned short *>(q) = (unsigned short)(u >> 16);
+}
 
 // OUT = false: the stretch's own contribution to the state only (the segments' first pass).  BWD: walks
 // that may have dots (w.dot), with the state's copy in two halves where they do.
@@ -257,25 +291,22 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto wait_gate = [&](int n) { return wait(&bars.gready[n % SLOTS], n / SLOTS); };
 
     if (warp == W_TMA) {
-        if (lane == 0) {
-            int n = 0;
-            for (; n < cnt; ++n) {
-                const int st = n % NS, c0 = chunk(n) * C;
-                if (n >= NS && !wait(&bars.free_s[st], n / NS - 1)) break;
-                uint8_t *s = base + st * K::STAGE;
+        const bool leader = elect();
+        int n = 0;
+        for (; n < cnt; ++n) {
+            const int st = n % NS, c0 = chunk(n) * C;
+            if (n >= NS && !wait(&bars.free_s[st], n / NS - 1)) break;
+            uint8_t *s = base + st * K::STAGE;
+            if (leader) {
                 tc::mbar_expect_tx(&bars.full[st], (OUT ? 2 : 1) * K::XB + K::ZB);
-#pragma unroll
-                for (int j = 0; j < A / 64; ++j) {
-                    if (OUT) tc::tma_load_3d(s + K::OFF_X + j * 8192, &maps.x[wi], &bars.full[st], j * 64, c0, bh);
-                    tc::tma_load_3d(s + K::OFF_Y + j * 8192, &maps.y[wi], &bars.full[st], j * 64, c0, bh);
-                }
-#pragma unroll
-                for (int j = 0; j < B / 64; ++j)
-                    tc::tma_load_3d(s + K::OFF_Z + j * 8192, &maps.z[wi], &bars.full[st], j * 64, c0, bh);
+                tc::tma_load_4d(s + K::OFF_Y, &maps.y[wi], &bars.full[st], 0, c0, 0, bh);
+                if (OUT) tc::tma_load_4d(s + K::OFF_X, &maps.x[wi], &bars.full[st], 0, c0, 0, bh);
+                tc::tma_load_4d(s + K::OFF_Z, &maps.z[wi], &bars.full[st], 0, c0, 0, bh);
             }
-            if (abort_flag)  // let this CTA's own copies land before it exits (bounded)
-                for (int m = n > NS ? n - NS : 0; m < n; ++m) tc::mbar_wait(&bars.full[m % NS], (m / NS) & 1, budget / 8);
+            __syncwarp();
         }
+        if (abort_flag)  // let this CTA's own copies land before it exits (bounded)
+            for (int m = n > NS ? n - NS : 0; m < n; ++m) tc::mbar_wait(&bars.full[m % NS], (m / NS) & 1, budget / 8);
     } else if (warp == W_STATE) {
         // The whole warp runs the loop and one elected lane issues, so that descriptors are warp-uniform.
         constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true), id_o1 = tc::idesc_bf16(B, 64, false, false);
@@ -398,7 +429,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const float up = exp2_sum(cc[e]), down = exp2_sum(cC - cc[e]);
                 sl.qw[2 * lane + e] = rev ? down : up;
                 sl.kw[2 * lane + e] = rev ? up : down;
-                sl.c2[2 * lane + e] = make_float2(cc[e].hi, cc[e].lo);
+                const Sum x = rev ? Sum{-cc[e].hi, -cc[e].lo} : cc[e];
+                sl.c2[2 * lane + e] = make_float2(x.hi, x.lo);
+                // the group is four lanes
+                const int src = rev ? lane & ~3 : lane | 3;
+                const Sum end = rev ? c.c0 : c.c1;
+                const Sum ce = {__shfl_sync(0xffffffffu, end.hi, src), __shfl_sync(0xffffffffu, end.lo, src)};
+                sl.gw[2 * lane + e] = exp2_sum(rev ? cc[e] - ce : ce - cc[e]);
             }
             if (lane == 0) sl.tot = exp2_sum(cC);
             __syncwarp();
@@ -418,13 +455,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float *kw = slots[n % SLOTS].kw;
 #pragma unroll 2
             for (int i = gtid; i < K::XB / 16; i += 128) {  // 8 pieces of 16 bytes a row of a 64-column slab
-                const float f = kw[(i >> 3) & 63];
+                const F2 f = f2(kw[(i >> 3) & 63], kw[(i >> 3) & 63]);
                 const uint4 u = y[i];
                 uint4 h, l;
-                split2(f * bf_lo(u.x), f * bf_hi(u.x), h.x, l.x);
-                split2(f * bf_lo(u.y), f * bf_hi(u.y), h.y, l.y);
-                split2(f * bf_lo(u.z), f * bf_hi(u.z), h.z, l.z);
-                split2(f * bf_lo(u.w), f * bf_hi(u.w), h.w, l.w);
+                split2(f * f2(bf_lo(u.x), bf_hi(u.x)), h.x, l.x);
+                split2(f * f2(bf_lo(u.y), bf_hi(u.y)), h.y, l.y);
+                split2(f * f2(bf_lo(u.z), bf_hi(u.z)), h.z, l.z);
+                split2(f * f2(bf_lo(u.w), bf_hi(u.w)), h.w, l.w);
                 hi[i] = h;
                 lo[i] = l;
             }
@@ -433,49 +470,68 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (wg == 1) {
         // ---------------------------------------------------------- D o P
-        // a thread holds rows r and r + 8 of its warp's 16, two columns of every eight
-        const int r = 16 * warp - 64 + (lane >> 2), cq = 2 * (lane & 3);
+        // A warp's 16 rows; a thread holds rows r and r + 8, two columns of every eight.  The warp's diagonal
+        // block (16 x 16) takes 2^(c_row - c_column) itself; the blocks on the diagonal's on side take it as
+        // 2^(c_row - c_end) 2^(c_end - c_column), end the last token (in walking order) of a column's group of
+        // eight: neither factor grows, and the second is made once a chunk.  The off side stays zero.
+        const int r0 = 16 * (warp & 3), r = r0 + (lane >> 2), cq = 2 * (lane & 3);
         uint8_t *pt = base + K::OFF_P;
+        if (OUT) {
+#pragma unroll 1
+            for (int c = rev ? 0 : 2 * (warp & 3) + 2; c < (rev ? 2 * (warp & 3) : 8); ++c)
+                *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r0 + (lane & 15), c)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        const int on0 = rev ? r0 + 16 : 0, on1 = rev ? 64 : r0;  // columns of the on side's blocks
         for (int n = 0; OUT && n < cnt; ++n) {
             if (!wait_gate(n) || !wait(&bars.pdone[n % K::NP], n / K::NP)) break;
             tc::tc_fence_after();
             const Slot &sl = slots[n % SLOTS];
             const float2 ca = sl.c2[r], cb = sl.c2[r + 8];
-            bool ok = true;
-#pragma unroll 1
-            for (int h = 0; h < 64; h += 32) {
-                float v[16];
-                tmem_ld_16x256(tmem + lane_base + K::T_P + (n % K::NP) * 64 + h, v);
-                uint32_t u[8];
+            const uint32_t tp = tmem + lane_base + K::T_P + (n % K::NP) * 64;
+            uint32_t u[4];
+            {
+                float v[8];
+                tmem_ld_16x256(tp + r0, v);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int c = h + 8 * k + cq;
+                for (int k = 0; k < 2; ++k) {
+                    const int c = r0 + 8 * k + cq;
                     const float4 cc = *reinterpret_cast<const float4 *>(&sl.c2[c]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {  // row r + 8 e, columns c and c + 1
                         const float2 cr = e ? cb : ca;
-                        float d0 = (cr.x - cc.x) + (cr.y - cc.y), d1 = (cr.x - cc.z) + (cr.y - cc.w);
-                        int a0 = r + 8 * e - c;  // column c is on where a0 >= 0 (forwards) or <= 0
-                        int a1 = a0 - 1;
-                        if (rev) {
-                            d0 = -d0; d1 = -d1;
-                            a0 = -a0; a1 = -a1;
-                        }
-                        u[2 * k + e] = tc::pack_bf16(a0 >= 0 ? v[4 * k + 2 * e] * ex2(d0) : 0.f,
-                                                     a1 >= 0 ? v[4 * k + 2 * e + 1] * ex2(d1) : 0.f);
+                        const int a = rev ? c - r - 8 * e : r + 8 * e - c, a1 = rev ? a + 1 : a - 1;  // on where >= 0
+                        const float x0 = (cr.x - cc.x) + (cr.y - cc.y), x1 = (cr.x - cc.z) + (cr.y - cc.w);
+                        u[2 * k + e] = tc::pack_bf16(a >= 0 ? v[4 * k + 2 * e] * ex2(x0) : 0.f,
+                                                     a1 >= 0 ? v[4 * k + 2 * e + 1] * ex2(x1) : 0.f);
                     }
                 }
-                if (h == 0 && n > 0) {  // the tile's last reader
-                    ok = wait(&bars.o2done, n - 1);
-                    if (!ok) break;
-                }
+            }
+            if (n > 0 && !wait(&bars.o2done, n - 1)) break;  // the tile's last reader
+            auto store = [&](int c0) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 2; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<uint32_t *>(pt + tc::sw128_off(r + 8 * e, (h >> 3) + k) + 2 * cq) = u[2 * k + e];
+                        *reinterpret_cast<uint32_t *>(pt + tc::sw128_off(r + 8 * e, (c0 >> 3) + k) + 2 * cq) = u[2 * k + e];
+            };
+            store(r0);
+#pragma unroll 1
+            for (int c0 = on0; c0 < on1; c0 += 16) {
+                float v[8];
+                tmem_ld_16x256(tp + c0, v);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float2 ce = sl.c2[c0 + 8 * k + (rev ? 0 : 7)];
+                    const F2 f = *reinterpret_cast<const F2 *>(&sl.gw[c0 + 8 * k + cq]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 cr = e ? cb : ca;
+                        const float x = ex2((cr.x - ce.x) + (cr.y - ce.y));
+                        u[2 * k + e] = pack(f2(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]) * (f2(x, x) * f));
+                    }
+                }
+                store(c0);
             }
-            if (!ok) break;
             tc::fence_async_smem();
             warp_arrive(&bars.p_ready, lane);
         }
@@ -505,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars.gfree[(n - 1) % SLOTS]);
             }
-            const float tot = slots[n % SLOTS].tot;
+            const F2 tot2 = f2(slots[n % SLOTS].tot, slots[n % SLOTS].tot);
             if (OUT && n > 0) {  // the copy's last reader
                 ok = wait(&bars.d1done, n - 1);
                 if (!ok) break;
@@ -518,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (OUT) {
                     uint32_t h[16], l[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) split2(v[2 * i], v[2 * i + 1], h[i], l[i]);
+                    for (int i = 0; i < 16; ++i) split2(f2(v[2 * i], v[2 * i + 1]), h[i], l[i]);
                     tmem_st16(tmem + lane_base + K::T_H + cb / 2, h);
                     if (BWD && split) tmem_st16(tmem + lane_base + K::T_L + cb / 2, l);
                 }
@@ -526,7 +582,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 32; e += 16) {
                     uint32_t u[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(v[e + i] * tot);
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 t = unpack(tot2 * f2(v[e + i], v[e + i + 1]));
+                        u[i] = __float_as_uint(t.x);
+                        u[i + 1] = __float_as_uint(t.y);
+                    }
                     tmem_st16(tmem + lane_base + K::T_S + cb + e, u);
                 }
             }
@@ -575,17 +635,23 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(qw + e + i);
-                    v[e + i] = fmaf(f.x, a[i], b[i]); v[e + i + 1] = fmaf(f.y, a[i + 1], b[i + 1]);
-                    v[e + i + 2] = fmaf(f.z, a[i + 2], b[i + 2]); v[e + i + 3] = fmaf(f.w, a[i + 3], b[i + 3]);
+                    const float2 x = unpack(fma2(f2(f.x, f.y), f2(a[i], a[i + 1]), f2(b[i], b[i + 1])));
+                    const float2 y = unpack(fma2(f2(f.z, f.w), f2(a[i + 2], a[i + 3]), f2(b[i + 2], b[i + 3])));
+                    v[e + i] = x.x; v[e + i + 1] = x.y; v[e + i + 2] = y.x; v[e + i + 3] = y.y;
                 }
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
             if (j >= 0) {
                 TO *out = static_cast<TO *>(w.out) + row0 * B + j;
+                if (cl == 32) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i < cl) put(out + i * B, v[i]);
+                    for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < cl) put(out + i * B, v[i]);
+                }
             }
             if (BWD && split) {
 #pragma unroll
@@ -622,8 +688,8 @@ cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, int nseg, float *s
     Maps maps;
     for (int i = 0; i < ws.n; ++i) {
         const Walk &w = ws.w[i];
-        if (!tmap::make_3d(&maps.x[i], w.x, w.a, L, BH, 64, C) || !tmap::make_3d(&maps.y[i], w.y, w.a, L, BH, 64, C) ||
-            !tmap::make_3d(&maps.z[i], w.z, w.b, L, BH, 64, C))
+        if (!tmap::make_slabs(&maps.x[i], w.x, w.a / 64, L, BH, C) || !tmap::make_slabs(&maps.y[i], w.y, w.a / 64, L, BH, C) ||
+            !tmap::make_slabs(&maps.z[i], w.z, w.b / 64, L, BH, C))
             return cudaErrorInvalidValue;
     }
     const int a = ws.w[0].a, b = ws.w[0].b;
