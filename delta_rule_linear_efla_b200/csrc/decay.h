@@ -35,8 +35,19 @@ struct Gate {
     int H;
 };
 
-// One walk.  seg: where the states that enter its segments are kept ([BH][nseg][a][b] fp32; unused
-// with one segment).  dotx / dot: where dot is given, each token's dotx_t . out_t before out is
+// A long sequence with few heads is cut into n segments, walked at the same time: a first pass gives the
+// stretches' own contributions to the state (u) and their whole decays (e), a second kernel chains them to
+// the states that enter the segments (in), and the walk proper follows.  fine: stretches of the first pass
+// in a segment (it has one segment less to do, and much less to do in it).
+struct Segments {
+    int n = 1, fine = 1;
+    int chunks;        // chunks in a segment, a multiple of fine
+    float *e;          // [2][BH][(n - 1) fine]: forward walks, backward walks
+    int stretches() const { return (n - 1) * fine; }
+};
+
+// One walk.  u, in: [BH][(n - 1) fine][a][b] and [BH][n][a][b] fp32, in walking order (unused with one
+// segment).  dotx / dot: where dot is given, each token's dotx_t . out_t before out is
 // rounded, as shares of the column blocks ([blocks][BH][L] fp32, added by the gradient kernel).
 struct Walk {
     const void *x, *y, *z;
@@ -47,7 +58,7 @@ struct Walk {
     int a, b, rev;
     const void *dotx;
     float *dot;
-    float *seg;
+    float *u, *in;
 };
 
 constexpr int MAX_WALKS = 3;
@@ -61,22 +72,22 @@ constexpr float L_MIN = -200.f;   // e^L_MIN is 0 in fp32: lower log-decays (-in
 
 // CUDA-core walks: any a, b <= 128, fp32 arithmetic; blocks of SIMT_BT value columns.
 constexpr int SIMT_BT = 32;
-int simt_segments(int BH, int L, const int *blocks, int n);
-cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool in_bf16,
-                              bool out_bf16, cudaStream_t s);
+Segments simt_segments(int BH, int L, const int *blocks, int n);
+cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool in_bf16, bool out_bf16,
+                              cudaStream_t s);
 
 // Tensor-core walks (decay_tc.cu): bf16 inputs, a and b of 64 or 128, x, y and z 16-byte aligned.  bwd: walks
 // with dots, given as DOT_PLANES shares (one for each warp of the output group); outputs are bf16.
 constexpr int DOT_PLANES = 4;
 bool tc_sizes(int dk, int dv, bool in_bf16);
-int tc_segments(int BH, int L, int n);
-cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out_bf16, bool bwd,
+Segments tc_segments(int BH, int L, int n);
+cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out_bf16, bool bwd,
                             cudaStream_t s);
 cudaError_t read_and_clear_error(unsigned int *out);
 
-// States of the segments: from every segment's own contribution (in seg, in walking order) and its
-// whole decay e^{sum l} (seg_e [BH][nseg]) to the state that enters it.
-cudaError_t launch_seg_chain(const Walks &ws, const float *seg_e, int BH, int nseg, cudaStream_t s);
+// The states that enter the segments: S_0 the state that enters the walk, S_{i+1} = e_i S_i + u_i over the
+// stretches.
+cudaError_t launch_seg_chain(const Walks &ws, const Segments &sg, int BH, cudaStream_t s);
 
 // dl from the walks' dots: dotq [nq][BH][L], dotk [nk][BH][L] (shares of their column blocks);
 // dS_final [BH][dk][dv] and the forward walk's end state S_end [BH][dv][dk], or both null.
@@ -85,6 +96,23 @@ cudaError_t launch_dlog(const float *dotq, int nq, const float *dotk, int nk, co
 
 cudaError_t launch_step(const void *q, const void *k, const void *v, Gate g, float *S, void *o, int BH, int dk,
                         int dv, bool in_bf16, bool o_bf16, cudaStream_t s);
+
+// Launches a kernel that begins with cudaGridDependencySynchronize(): it is set up while the kernel before
+// it in the stream ends.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
 
 }  // namespace decay
 }  // namespace efla

@@ -9,6 +9,7 @@
 namespace {
 
 using efla::decay::Gate;
+using efla::decay::Segments;
 using efla::decay::Walk;
 using efla::decay::Walks;
 
@@ -42,37 +43,40 @@ struct Arena {
 int blocks_of(int b) { return (b + efla::decay::SIMT_BT - 1) / efla::decay::SIMT_BT; }
 
 // The walks' segments and their states: lays them out in the arena.
-int plan_segments(Walks &ws, int BH, int L, bool tc, Arena &ar, float **seg_e) {
+Segments plan_segments(Walks &ws, int BH, int L, bool tc, Arena &ar) {
     int blocks[efla::decay::MAX_WALKS];
     for (int i = 0; i < ws.n; ++i) blocks[i] = blocks_of(ws.w[i].b);
-    const int nseg = tc ? efla::decay::tc_segments(BH, L, ws.n) : efla::decay::simt_segments(BH, L, blocks, ws.n);
-    *seg_e = nullptr;
-    if (nseg > 1) {
-        for (int i = 0; i < ws.n; ++i) ws.w[i].seg = ar.floats((size_t)BH * nseg * ws.w[i].a * ws.w[i].b);
-        *seg_e = ar.floats((size_t)2 * BH * nseg);
+    Segments sg = tc ? efla::decay::tc_segments(BH, L, ws.n) : efla::decay::simt_segments(BH, L, blocks, ws.n);
+    if (sg.n > 1) {
+        for (int i = 0; i < ws.n; ++i) {
+            const size_t ab = (size_t)ws.w[i].a * ws.w[i].b;
+            ws.w[i].u = ar.floats(BH * sg.stretches() * ab);
+            ws.w[i].in = ar.floats(BH * sg.n * ab);
+        }
+        sg.e = ar.floats((size_t)2 * BH * sg.stretches());
     }
-    return nseg;
+    return sg;
 }
 
 struct FwdPlan {
     Walks ws{};
-    float *seg_e = nullptr;
-    int nseg = 1;
+    Segments sg;
     size_t bytes = 0;
     FwdPlan(int BH, int L, int dk, int dv, bool tc, void *base) {
         Arena ar{static_cast<char *>(base)};
         ws.n = 1;
         ws.w[0].a = dk;
         ws.w[0].b = dv;
-        nseg = plan_segments(ws, BH, L, tc, ar, &seg_e);
+        sg = plan_segments(ws, BH, L, tc, ar);
         bytes = ar.used;
     }
 };
 
 struct BwdPlan {
     Walks ws{};  // dq, dk, dv
-    float *seg_e = nullptr, *S_end = nullptr, *dotq = nullptr, *dotk = nullptr;
-    int nseg = 1, planes = 1;
+    Segments sg;
+    float *S_end = nullptr, *dotq = nullptr, *dotk = nullptr;
+    int planes = 1;
     size_t bytes = 0;
     BwdPlan(int BH, int L, int dk, int dv, bool tc, void *base) {
         Arena ar{static_cast<char *>(base)};
@@ -84,7 +88,7 @@ struct BwdPlan {
         dotq = ar.floats((size_t)planes * BH * L);
         dotk = ar.floats((size_t)planes * BH * L);
         S_end = ar.floats((size_t)BH * dk * dv);
-        nseg = plan_segments(ws, BH, L, tc, ar, &seg_e);
+        sg = plan_segments(ws, BH, L, tc, ar);
         bytes = ar.used;
     }
 };
@@ -137,8 +141,8 @@ efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, co
     w.out = o;
     w.s_end = S_final;
     const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
-    if (tc) return from_cuda(efla::decay::launch_walks_tc(p.ws, g, BH, L, p.nseg, p.seg_e, o_dt == EFLA_BF16, false, s));
-    return from_cuda(efla::decay::launch_walks_simt(p.ws, g, BH, L, p.nseg, p.seg_e, dt == EFLA_BF16,
+    if (tc) return from_cuda(efla::decay::launch_walks_tc(p.ws, g, BH, L, p.sg, o_dt == EFLA_BF16, false, s));
+    return from_cuda(efla::decay::launch_walks_simt(p.ws, g, BH, L, p.sg, dt == EFLA_BF16,
                                                     o_dt == EFLA_BF16, s));
 }
 
@@ -193,8 +197,8 @@ efla_status efla_decay_bwd(const void *q, const void *k, const void *v, const vo
     }
     const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
     const bool bf16 = dt == EFLA_BF16;
-    const cudaError_t e = tc ? efla::decay::launch_walks_tc(p.ws, g, BH, L, p.nseg, p.seg_e, bf16, true, s)
-                             : efla::decay::launch_walks_simt(p.ws, g, BH, L, p.nseg, p.seg_e, bf16, bf16, s);
+    const cudaError_t e = tc ? efla::decay::launch_walks_tc(p.ws, g, BH, L, p.sg, bf16, true, s)
+                             : efla::decay::launch_walks_simt(p.ws, g, BH, L, p.sg, bf16, bf16, s);
     if (e != cudaSuccess || !want_dl) return from_cuda(e);
     return from_cuda(efla::decay::launch_dlog(p.dotq, p.planes, p.dotk, p.planes, dS_final, tail ? p.S_end : nullptr, g, dlog_g,
                                               BH, L, dk, dv, s));

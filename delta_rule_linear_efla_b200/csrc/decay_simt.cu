@@ -80,8 +80,7 @@ __device__ __forceinline__ void fma4(float (&acc)[4], float s, const float4 &v) 
 // OUT = false: the stretch's own contribution to the state only (segments' first pass).
 template <typename T, typename TO, bool OUT>
 __global__ void __launch_bounds__(NT, 2)
-    walk_simt_kernel(const __grid_constant__ Walks ws, const Gate g, int BH, int L, int nseg, int seg_chunks,
-                     float *__restrict__ seg_e) {
+    walk_simt_kernel(const __grid_constant__ Walks ws, const __grid_constant__ Segments sg, const Gate g, int BH, int L) {
     extern __shared__ __align__(16) float sm[];
     // ---- which walk, column block and head: blockIdx.x = (block of all walks) * BH + bh
     const int bh = blockIdx.x % BH;
@@ -100,13 +99,14 @@ __global__ void __launch_bounds__(NT, 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int NC = (L + C - 1) / C;
     const int seg = blockIdx.y;  // in walking order
-    const int i0 = seg * seg_chunks, i1 = min(NC, i0 + seg_chunks);
+    const int i0 = seg * sg.chunks, i1 = min(NC, i0 + sg.chunks);
+    if (OUT) cudaGridDependencySynchronize();
 
     // ---- the state that enters
     const size_t sbh = (size_t)bh * a * b;
     const float *sin = nullptr;
-    if (OUT) sin = nseg > 1 ? w.seg + ((size_t)bh * nseg + seg) * a * b : (w.s0 ? w.s0 + sbh : nullptr);
-    const bool st = nseg == 1 && w.s0_t;
+    if (OUT) sin = sg.n > 1 ? w.in + ((size_t)bh * sg.n + seg) * a * b : (w.s0 ? w.s0 + sbh : nullptr);
+    const bool st = sg.n == 1 && w.s0_t;
     for (int e = tid; e < ap * BT; e += NT) {
         const int i = e / BT, j = e % BT;
         float v = 0.f;
@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(NT, 2)
     }
     __syncthreads();
     float *sout = nullptr;
-    if (!OUT) sout = w.seg + ((size_t)bh * nseg + seg) * a * b;
-    else if (seg == nseg - 1 && w.s_end) sout = w.s_end + sbh;
+    if (!OUT) sout = w.u + ((size_t)bh * (sg.n - 1) + seg) * a * b;
+    else if (seg == sg.n - 1 && w.s_end) sout = w.s_end + sbh;
     if (sout) {
         for (int e = tid; e < a * BT; e += NT) {
             const int i = e / BT, j = e % BT;
@@ -270,51 +270,80 @@ __global__ void __launch_bounds__(NT, 2)
     }
     // every walk in the same direction finds the same decay of a segment: its first one writes it
     if (!OUT && warp == 0 && lane == 0 && blk == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
-        seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp2_sum(seg_sum);
+        sg.e[((size_t)(rev ? 1 : 0) * BH + bh) * (sg.n - 1) + seg] = exp2_sum(seg_sum);
 }
 
 template <typename T, typename TO>
-cudaError_t launch_t(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, cudaStream_t s) {
+cudaError_t launch_t(const Walks &ws, Gate g, int BH, int L, const Segments &sg, cudaStream_t s) {
     int blocks = 0, smem = 0;
     for (int i = 0; i < ws.n; ++i) {
         blocks += (ws.w[i].b + BT - 1) / BT;
         const int t = Lay(ws.w[i].a).total;
         smem = t > smem ? t : smem;
     }
-    const int NC = (L + C - 1) / C, per = (NC + nseg - 1) / nseg;
     auto *full = walk_simt_kernel<T, TO, true>;
     auto *part = walk_simt_kernel<T, TO, false>;
     cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && nseg > 1) e = cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && sg.n > 1) e = cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    if (nseg > 1) {
-        part<<<dim3(blocks * BH, nseg - 1), NT, smem, s>>>(ws, g, BH, L, nseg, per, seg_e);
+    if (sg.n == 1) {
+        full<<<dim3(blocks * BH), NT, smem, s>>>(ws, sg, g, BH, L);
         count_launches(1);
-        e = cudaGetLastError();
-        if (e == cudaSuccess) e = launch_seg_chain(ws, seg_e, BH, nseg, s);
-        if (e != cudaSuccess) return e;
+        return cudaGetLastError();
     }
-    full<<<dim3(blocks * BH, nseg), NT, smem, s>>>(ws, g, BH, L, nseg, per, seg_e);
+    part<<<dim3(blocks * BH, sg.n - 1), NT, smem, s>>>(ws, sg, g, BH, L);
     count_launches(1);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_seg_chain(ws, sg, BH, s);
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+    return launch_after(full, dim3(blocks * BH, sg.n), NT, smem, s, ws, sg, g, BH, L);
 }
 
-// One thread per state element: S_0 is the state that enters the walk, S_{i+1} = e_i S_i + U_i; U_i is
-// read from where S_i is written.
-__global__ void __launch_bounds__(256)
-    seg_chain_kernel(const __grid_constant__ Walks ws, const float *__restrict__ seg_e, int BH, int nseg) {
+// One thread per VEC state elements.
+template <int VEC>
+__global__ void __launch_bounds__(128)
+    seg_chain_kernel(const __grid_constant__ Walks ws, const __grid_constant__ Segments sg, int BH) {
+    cudaGridDependencySynchronize();
     const Walk &w = ws.w[blockIdx.z];
-    const int ab = w.a * w.b, bh = blockIdx.x;
-    const float *ee = seg_e + ((size_t)(w.rev ? 1 : 0) * BH + bh) * nseg;
-    for (int e = blockIdx.y * 256 + threadIdx.x; e < ab; e += gridDim.y * 256) {
-        const int i = e / w.b, j = e - i * w.b;
-        float s = w.s0 ? w.s0[(size_t)bh * ab + (w.s0_t ? j * w.a + i : e)] : 0.f;
-        float *p = w.seg + (size_t)bh * nseg * ab + e;
-        for (int k = 0; k < nseg; ++k) {
-            const float u = k + 1 < nseg ? p[(size_t)k * ab] : 0.f;
-            p[(size_t)k * ab] = s;
-            if (k + 1 < nseg) s = fmaf(ee[k], s, u);
-        }
+    const int ab = w.a * w.b, bh = blockIdx.x, e0 = (blockIdx.y * 128 + threadIdx.x) * VEC, nf = (sg.n - 1) * sg.fine;
+    if (e0 >= ab) return;
+    const float *ee = sg.e + ((size_t)(w.rev ? 1 : 0) * BH + bh) * nf;
+    const float *u = w.u + (size_t)bh * nf * ab + e0;
+    float *in = w.in + (size_t)bh * sg.n * ab + e0;
+    float s[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const int x = (e0 + i) / w.b, y = (e0 + i) - x * w.b;
+        s[i] = w.s0 ? w.s0[(size_t)bh * ab + (w.s0_t ? y * w.a + x : e0 + i)] : 0.f;
+    }
+    auto store = [&](int k) {
+        if constexpr (VEC == 4) *reinterpret_cast<float4 *>(in + (size_t)k * ab) = make_float4(s[0], s[1], s[2], s[3]);
+        else in[(size_t)k * ab] = s[0];
+    };
+    store(0);
+    constexpr int AHEAD = 4;
+    for (int f0 = 0; f0 < nf; f0 += AHEAD) {
+        float v[AHEAD][VEC], f[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (f0 + k < nf) {
+                f[k] = ee[f0 + k];
+                const float *p = u + (size_t)(f0 + k) * ab;
+                if constexpr (VEC == 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(p);
+                    v[k][0] = t.x; v[k][1] = t.y; v[k][2] = t.z; v[k][3] = t.w;
+                } else {
+                    v[k][0] = *p;
+                }
+            }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (f0 + k < nf) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) s[i] = fmaf(f[k], s[i], v[k][i]);
+                if ((f0 + k + 1) % sg.fine == 0) store((f0 + k + 1) / sg.fine);
+            }
     }
 }
 
@@ -330,6 +359,7 @@ __global__ void __launch_bounds__(DL_T)
     __shared__ double part[DL_T / 32];
     __shared__ double carry_s;
     const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    cudaGridDependencySynchronize();
     double carry = 0.0;
     if (dS) {  // <dS_final, S_final>
         const size_t base = (size_t)bh * dk * dv;
@@ -388,44 +418,51 @@ __global__ void __launch_bounds__(DL_T)
 
 }  // namespace
 
-int simt_segments(int BH, int L, const int *blocks, int n) {
+Segments simt_segments(int BH, int L, const int *blocks, int n) {
     // A segment run more costs about a third of a walk (the state update alone); below about one CTA
     // an SM the sequence is cut until the device is full, at four chunks a segment or more.
+    Segments sg{};
     long long ctas = 0;
     for (int i = 0; i < n; ++i) ctas += (long long)blocks[i] * BH;
     const int NC = (L + C - 1) / C;
-    if (ctas >= 148 || NC < 8) return 1;
+    sg.chunks = NC;
+    if (ctas >= 148) return sg;
     long long want = (2 * 148 + ctas - 1) / ctas;
     if (want > NC / 4) want = NC / 4;
-    if (want < 2) return 1;
-    const int per = (int)((NC + want - 1) / want);
-    return (NC + per - 1) / per;
+    if (want < 2) return sg;
+    sg.chunks = (int)((NC + want - 1) / want);
+    sg.n = (NC + sg.chunks - 1) / sg.chunks;
+    return sg;
 }
 
-cudaError_t launch_seg_chain(const Walks &ws, const float *seg_e, int BH, int nseg, cudaStream_t s) {
+cudaError_t launch_seg_chain(const Walks &ws, const Segments &sg, int BH, cudaStream_t s) {
     int ab = 1;
-    for (int i = 0; i < ws.n; ++i) ab = ws.w[i].a * ws.w[i].b > ab ? ws.w[i].a * ws.w[i].b : ab;
-    seg_chain_kernel<<<dim3(BH, (ab + 255) / 256, ws.n), 256, 0, s>>>(ws, seg_e, BH, nseg);
+    bool vec = true;
+    for (int i = 0; i < ws.n; ++i) {
+        const int n = ws.w[i].a * ws.w[i].b;
+        ab = n > ab ? n : ab;
+        vec = vec && n % 4 == 0;
+    }
     count_launches(1);
-    return cudaGetLastError();
+    if (vec) return launch_after(seg_chain_kernel<4>, dim3(BH, (ab + 511) / 512, ws.n), 128, 0, s, ws, sg, BH);
+    return launch_after(seg_chain_kernel<1>, dim3(BH, (ab + 127) / 128, ws.n), 128, 0, s, ws, sg, BH);
 }
 
-cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool in_bf16,
-                              bool out_bf16, cudaStream_t s) {
+cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool in_bf16, bool out_bf16,
+                              cudaStream_t s) {
     using bf = __nv_bfloat16;
-    if (in_bf16)
-        return out_bf16 ? launch_t<bf, bf>(ws, g, BH, L, nseg, seg_e, s) : launch_t<bf, float>(ws, g, BH, L, nseg, seg_e, s);
-    return out_bf16 ? launch_t<float, bf>(ws, g, BH, L, nseg, seg_e, s) : launch_t<float, float>(ws, g, BH, L, nseg, seg_e, s);
+    if (in_bf16) return out_bf16 ? launch_t<bf, bf>(ws, g, BH, L, sg, s) : launch_t<bf, float>(ws, g, BH, L, sg, s);
+    return out_bf16 ? launch_t<float, bf>(ws, g, BH, L, sg, s) : launch_t<float, float>(ws, g, BH, L, sg, s);
 }
 
 cudaError_t launch_dlog(const float *dotq, int nq, const float *dotk, int nk, const float *dS_final,
                         const float *S_end, Gate g, void *dlog, int BH, int L, int dk, int dv, cudaStream_t s) {
-    if (g.bf16)
-        dlog_kernel<__nv_bfloat16><<<BH, DL_T, 0, s>>>(dotq, nq, dotk, nk, dS_final, S_end, g, (__nv_bfloat16 *)dlog, BH, L, dk, dv);
-    else
-        dlog_kernel<float><<<BH, DL_T, 0, s>>>(dotq, nq, dotk, nk, dS_final, S_end, g, (float *)dlog, BH, L, dk, dv);
     count_launches(1);
-    return cudaGetLastError();
+    if (g.bf16)
+        return launch_after(dlog_kernel<__nv_bfloat16>, dim3(BH), DL_T, 0, s, dotq, nq, dotk, nk, dS_final, S_end, g,
+                            (__nv_bfloat16 *)dlog, BH, L, dk, dv);
+    return launch_after(dlog_kernel<float>, dim3(BH), DL_T, 0, s, dotq, nq, dotk, nk, dS_final, S_end, g, (float *)dlog, BH,
+                        L, dk, dv);
 }
 
 }  // namespace decay

@@ -64,23 +64,24 @@ struct Cfg {
     static constexpr int OFF_P = OFF_W + 4 * XB;    // D o P
     static constexpr int SMEM = OFF_P + 8192 + 1024;  // + alignment slack
     // tensor memory columns
-    // buffers of P, and of O1^T and O2^T: a second one of the outputs first (their loop, from free through
-    // two products to done and read, is the longer one)
-    static constexpr int NO = BWD && A == 128 ? 1 : 2, NP = A == 128 && !BWD ? 1 : 2;
-    static constexpr uint32_t T_S = 0, T_H = A, T_L = T_H + A / 2, T_P = T_L + (BWD ? A / 2 : 0), T_O = T_P + NP * 64;
-    static_assert(T_O + NO * 128 <= 512, "tensor memory");
+    // P twice, so that the mask's loop does not wait for the next one; O1^T twice where it fits
+    static constexpr int NO1 = BWD && A == 128 ? 1 : 2;
+    static constexpr uint32_t T_S = 0, T_H = A, T_L = T_H + A / 2, T_P = T_L + (BWD ? A / 2 : 0), T_O1 = T_P + 128,
+                              T_O2 = T_O1 + NO1 * 64;
+    static_assert(T_O2 + 64 <= 512, "tensor memory");
 };
 
 struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
-    uint64_t full[NS], gready[SLOTS], y_free[2], pdone[2], d1done, d2done, o1done[2], o2done, o2done_b[2], drain[2];
+    uint64_t full[NS], gready[SLOTS], y_free[2], pdone[2], d1done, d2done, o1done[2], o2done, o2read, drain[2];
     // one arrival from each of four warps
-    uint64_t y_ready[2], p_ready, s_ready;
-    uint64_t gfree[SLOTS], o_free[2];  // eight warps with output, four without
+    uint64_t p_ready, s_ready;
+    uint64_t gfree[SLOTS], o_free[2];  // the eight output warps (without output, gfree: the weights' sixteen)
+    uint64_t y_ready[2];               // the weights' four warps, sixteen without output
     uint64_t free_s[NS];               // one from each issuer
 };
-constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + SLOTS + 2 + 2 + 2 + 2 + 1 + 2 + 2, BARS_FOUR = BARS_ONE + 4,
-              BARS_OUT = BARS_FOUR + SLOTS + 2;
+constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + SLOTS + 2 + 2 + 2 + 2 + 2 + 2, BARS_FOUR = BARS_ONE + 2,
+              BARS_OUT = BARS_FOUR + SLOTS + 2, BARS_Y = BARS_OUT + 2;
 
 struct Slot {
     float qw[C], kw[C];
@@ -247,8 +248,8 @@ __device__ __forceinline__ void put2(__nv_bfloat16 *p, __nv_bfloat16 *q, float x
 // that may have dots (w.dot), with the state's copy in two halves where they do.
 template <int A, int B, typename TO, bool OUT, bool BWD>
 __global__ void __launch_bounds__(THREADS, 1)
-    walk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Walks ws, const Gate g, int BH, int L,
-                   int nseg, int seg_chunks, float *__restrict__ seg_e) {
+    walk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Walks ws, const __grid_constant__ Segments sg,
+                   const Gate g, int BH, int L) {
     using K = Cfg<A, B, BWD>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = tc::smem_u32(smem_raw);
@@ -261,18 +262,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, gtid = tid & 127;
     // ---- blockIdx.x = (head, segment in walking order, walk)
     const int wi = blockIdx.x % ws.n, rest = blockIdx.x / ws.n;
-    const int segs = OUT ? nseg : nseg - 1;
+    const int segs = OUT ? sg.n : (sg.n - 1) * sg.fine, per = OUT ? sg.chunks : sg.chunks / sg.fine;
     const int seg = rest % segs, bh = rest / segs;
     const Walk &w = ws.w[wi];
     const bool rev = w.rev != 0, split = BWD && w.dot != nullptr;
     const int NC = (L + C - 1) / C;
-    const int i0 = seg * seg_chunks, cnt = min(NC, i0 + seg_chunks) - i0;
-    auto chunk = [&](int i) { return rev ? NC - 1 - (i0 + i) : i0 + i; };
+    const int i0 = seg * per, cnt = min(NC, i0 + per) - i0;
+    // Without output the state's weights are taken up to the segment's end, from its last chunk backwards, so
+    // that every product simply adds to the accumulator.
+    auto chunk = [&](int i) {
+        const int k = OUT ? i0 + i : i0 + cnt - 1 - i;
+        return rev ? NC - 1 - k : k;
+    };
 
     if (tid == 0) {
         uint64_t *b = reinterpret_cast<uint64_t *>(&bars);
         for (int i = 0; i < BARS; ++i) 
-            tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS_FOUR ? 4 : i < BARS_OUT ? (OUT ? 8 : 4) : (OUT ? 2 : 1));
+            tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS_FOUR ? 4 : i < BARS_OUT ? (OUT ? 8 : 16) : i < BARS_Y ? (OUT ? 4 : 16) : (OUT ? 2 : 1));
         tc::fence_mbar_init();
         abort_flag = 0;
         tc::tma_prefetch_desc(&maps.x[wi]);
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int st = 0, ph = 0;  // stage and its pass
         for (int n = 0; n < cnt; ++n) {
             const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-            if (!wait(&bars.full[st], ph) || !wait(&bars.y_ready[n & 1], n >> 1) || !wait(&bars.s_ready, n)) break;
+            if (!wait(&bars.full[st], ph) || !wait(&bars.y_ready[n & 1], n >> 1) || (OUT && !wait(&bars.s_ready, n))) break;
             tc::tc_fence_after();
             if (leader) {  // S^T += Z^T Yw
                 const uint64_t yw = dw + (uint64_t)((n & 1) * (2 * K::XB >> 4));
@@ -324,17 +330,18 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + (h * (K::XB >> 4) + kk * 128), id_s, 1u);
+                        tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + (h * (K::XB >> 4) + kk * 128), id_s,
+                                     OUT || n > 0 || h > 0 || kk > 0);
                 tc::mma_commit(&bars.d2done);
                 tc::mma_commit(&bars.y_free[n & 1]);
             }
             __syncwarp();
             if (OUT) {
-                const int ob = n % K::NO;
-                if (n >= K::NO && !wait(&bars.o_free[ob], n / K::NO - 1)) break;
+                const int ob = n % K::NO1, m = n - K::NO1;  // read by the output of chunk m
+                if (m >= 0 && !wait(&bars.o_free[m & 1], m >> 1)) break;
                 tc::tc_fence_after();
                 if (leader) {  // O1^T = S^T X^T
-                    const uint32_t o1 = tmem + K::T_O + ob * 128;
+                    const uint32_t o1 = tmem + K::T_O1 + ob * 64;
 #pragma unroll
                     for (int kk = 0; kk < A / 16; ++kk)
                         tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
@@ -346,7 +353,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                                            dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, 1u);
                     }
                     tc::mma_commit(&bars.d1done);
-                    tc::mma_commit(&bars.o1done[ob]);
+                    tc::mma_commit(&bars.o1done[n & 1]);
                 }
             }
             if (leader) tc::mma_commit(&bars.free_s[st]);
@@ -371,9 +378,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int kk = 0; kk < A / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
-                    tc::mma_bf16(tmem + K::T_P + (n % K::NP) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
+                    tc::mma_bf16(tmem + K::T_P + (n & 1) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
                 }
-                tc::mma_commit(&bars.pdone[n % K::NP]);
+                tc::mma_commit(&bars.pdone[n & 1]);
             }
             __syncwarp();
         };
@@ -385,23 +392,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                 st = 0;
                 ++ph;
             }
-            // P of the next chunk: with one buffer once the mask has read this one's
-            if (K::NP == 1 && !wait(&bars.p_ready, n)) break;
             if (n + 1 < cnt) {
                 if (!wait(&bars.full[st], ph)) break;
                 tc::tc_fence_after();
                 issue_p(n + 1, st);
             }
-            const int ob = n % K::NO;
-            if ((K::NP == 2 && !wait(&bars.p_ready, n)) || (n >= K::NO && !wait(&bars.o_free[ob], n / K::NO - 1))) break;
+            if (!wait(&bars.p_ready, n) || (n > 0 && !wait(&bars.o_free[(n - 1) & 1], (n - 1) >> 1))) break;
             tc::tc_fence_after();
             if (leader) {  // O2^T = Z^T (D o P)^T
                 const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc::mma_bf16(tmem + K::T_O + ob * 128 + 64, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
+                    tc::mma_bf16(tmem + K::T_O2, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
                 tc::mma_commit(&bars.o2done);
-                tc::mma_commit(&bars.o2done_b[ob]);
+                tc::mma_commit(&bars.o2read);
                 tc::mma_commit(&bars.free_s[cur]);
             }
             __syncwarp();
@@ -416,6 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int n = 0; n < cnt; ++n) {
             const PairSum c = chunk_sums(l0, l1, lane);
             const Sum cC = last_sum(c), cc[2] = {c.c0, c.c1};
+            const float after = OUT ? 1.f : exp2_sum(sum);  // the decay of the chunks already walked
             sum = sum + cC;
             if (n + 1 < cnt) {  // the next chunk's, while this one's weights are made
                 t = chunk(n + 1) * C + 2 * lane;
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int e = 0; e < 2; ++e) {
                 const float up = exp2_sum(cc[e]), down = exp2_sum(cC - cc[e]);
                 sl.qw[2 * lane + e] = rev ? down : up;
-                sl.kw[2 * lane + e] = rev ? up : down;
+                sl.kw[2 * lane + e] = (rev ? up : down) * (OUT ? 1.f : after);
                 const Sum x = rev ? Sum{-cc[e].hi, -cc[e].lo} : cc[e];
                 sl.c2[2 * lane + e] = make_float2(x.hi, x.lo);
                 // the group is four lanes
@@ -443,8 +448,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         // every walk in the same direction finds the same decay of a segment: its first one writes it
         if (!OUT && lane == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
-            seg_e[((size_t)(rev ? 1 : 0) * BH + bh) * nseg + seg] = exp2_sum(sum);
-    } else if (wg == 0) {
+            sg.e[((size_t)(rev ? 1 : 0) * BH + bh) * segs + seg] = exp2_sum(sum);
+    } else if (OUT ? wg == 0 : wg < 4) {
         // ---------------------------------------------------------- Yw
         for (int n = 0; n < cnt; ++n) {
             if (!wait_gate(n) || !wait(&bars.full[n % NS], n / NS)) break;
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             uint4 *lo = hi + K::XB / 16;
             const float *kw = slots[n % SLOTS].kw;
 #pragma unroll 2
-            for (int i = gtid; i < K::XB / 16; i += 128) {  // 8 pieces of 16 bytes a row of a 64-column slab
+            for (int i = OUT ? gtid : tid; i < K::XB / 16; i += OUT ? 128 : 512) {  // 8 pieces of 16 bytes a row of a 64-column slab
                 const F2 f = f2(kw[(i >> 3) & 63], kw[(i >> 3) & 63]);
                 const uint4 u = y[i];
                 uint4 h, l;
@@ -467,8 +472,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             tc::fence_async_smem();
             warp_arrive(&bars.y_ready[n & 1], lane);
+            if (!OUT && lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
         }
-    } else if (wg == 1) {
+        if (!OUT && wg == 0 && wait(&bars.drain[0], 0)) {  // the segment's contribution
+            const int j = acc_row<B>(warp, lane);
+            float *sout = w.u + ((size_t)bh * segs + seg) * A * B;
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int cb = 0; cb < A; cb += 16) {
+                float v[16];
+                tc::tmem_ld16(tmem + lane_base + K::T_S + cb, v);
+                if (j >= 0)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sout[(size_t)(cb + i) * B + j] = v[i];
+            }
+        }
+    } else if (OUT && wg == 1) {
         // ---------------------------------------------------------- D o P
         // A warp's 16 rows; a thread holds rows r and r + 8, two columns of every eight.  The warp's diagonal
         // block (16 x 16) takes 2^(c_row - c_column) itself; the blocks on the diagonal's on side take it as
@@ -476,18 +495,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         // eight: neither factor grows, and the second is made once a chunk.  The off side stays zero.
         const int r0 = 16 * (warp & 3), r = r0 + (lane >> 2), cq = 2 * (lane & 3);
         uint8_t *pt = base + K::OFF_P;
-        if (OUT) {
+        {
 #pragma unroll 1
             for (int c = rev ? 0 : 2 * (warp & 3) + 2; c < (rev ? 2 * (warp & 3) : 8); ++c)
                 *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r0 + (lane & 15), c)) = make_uint4(0u, 0u, 0u, 0u);
         }
         const int on0 = rev ? r0 + 16 : 0, on1 = rev ? 64 : r0;  // columns of the on side's blocks
-        for (int n = 0; OUT && n < cnt; ++n) {
-            if (!wait_gate(n) || !wait(&bars.pdone[n % K::NP], n / K::NP)) break;
+        for (int n = 0; n < cnt; ++n) {
+            if (!wait_gate(n) || !wait(&bars.pdone[n & 1], n >> 1)) break;
             tc::tc_fence_after();
             const Slot &sl = slots[n % SLOTS];
             const float2 ca = sl.c2[r], cb = sl.c2[r + 8];
-            const uint32_t tp = tmem + lane_base + K::T_P + (n % K::NP) * 64;
+            const uint32_t tp = tmem + lane_base + K::T_P + (n & 1) * 64;
             uint32_t u[4];
             {
                 float v[8];
@@ -535,13 +554,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::fence_async_smem();
             warp_arrive(&bars.p_ready, lane);
         }
-    } else if (wg == 2) {
+    } else if (OUT && wg == 2) {
         // ---------------------------------------------------------- S^T
         const int j = acc_row<B>(warp & 3, lane);
         const size_t ab = (size_t)A * B;
-        const float *sin = nullptr;
-        if (OUT) sin = nseg > 1 ? w.seg + ((size_t)bh * nseg + seg) * ab : (w.s0 ? w.s0 + bh * ab : nullptr);
-        const bool st = nseg == 1 && w.s0_t;
+        cudaGridDependencySynchronize();
+        const float *sin = sg.n > 1 ? w.in + ((size_t)bh * sg.n + seg) * ab : (w.s0 ? w.s0 + bh * ab : nullptr);
+        const bool st = sg.n == 1 && w.s0_t;
         bool ok = true;
         {  // the state that enters, as if a chunk had left it
 #pragma unroll 1
@@ -557,12 +576,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = wait_gate(n) && (n == 0 || wait(&bars.d2done, n - 1));
             if (!ok) break;
             tc::tc_fence_after();
-            if (!OUT && n > 0) {  // the weights of the chunk before are read (its Yw was)
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bars.gfree[(n - 1) % SLOTS]);
-            }
             const F2 tot2 = f2(slots[n % SLOTS].tot, slots[n % SLOTS].tot);
-            if (OUT && n > 0) {  // the copy's last reader
+            if (n > 0) {  // the copy's last reader
                 ok = wait(&bars.d1done, n - 1);
                 if (!ok) break;
                 tc::tc_fence_after();
@@ -571,13 +586,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int cb = 0; cb < A; cb += 32) {
                 float v[32];
                 tc::tmem_ld32(tmem + lane_base + K::T_S + cb, v);
-                if (OUT) {
-                    uint32_t h[16], l[16];
+                uint32_t h[16], l[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) split2(f2(v[2 * i], v[2 * i + 1]), h[i], l[i]);
-                    tmem_st16(tmem + lane_base + K::T_H + cb / 2, h);
-                    if (BWD && split) tmem_st16(tmem + lane_base + K::T_L + cb / 2, l);
-                }
+                for (int i = 0; i < 16; ++i) split2(f2(v[2 * i], v[2 * i + 1]), h[i], l[i]);
+                tmem_st16(tmem + lane_base + K::T_H + cb / 2, h);
+                if (BWD && split) tmem_st16(tmem + lane_base + K::T_L + cb / 2, l);
 #pragma unroll
                 for (int e = 0; e < 32; e += 16) {
                     uint32_t u[16];
@@ -593,9 +606,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             warp_arrive(&bars.s_ready, lane);
         }
-        float *sout = nullptr;
-        if (!OUT) sout = w.seg + ((size_t)bh * nseg + seg) * ab;
-        else if (seg == nseg - 1 && w.s_end) sout = w.s_end + bh * ab;
+        float *sout = seg == sg.n - 1 && w.s_end ? w.s_end + bh * ab : nullptr;
         if (ok && sout && wait(&bars.d2done, cnt - 1)) {
             tc::tc_fence_after();
 #pragma unroll 1
@@ -611,7 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---------------------------------------------------------- out
         const int j = acc_row<B>(warp & 3, lane), h0 = wg == 3 ? 0 : 32;  // tokens h0 .. h0 + 31 of a chunk
         for (int n = 0; n < cnt; ++n) {
-            const int t0 = chunk(n) * C + h0, cl = min(32, L - t0), ob = n % K::NO;
+            const int t0 = chunk(n) * C + h0, cl = min(32, L - t0);
             const size_t row0 = (size_t)bh * L + t0;
             uint32_t xr[16];  // this lane's elements of the dots' other factor, two tokens a word
             if (BWD && split) {
@@ -622,16 +633,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                     xr[i] = a | (b << 16);
                 }
             }
-            if (!wait_gate(n) || !wait(&bars.o1done[ob], n / K::NO) || !wait(&bars.o2done_b[ob], n / K::NO)) break;
+            if (!wait_gate(n) || !wait(&bars.o1done[n & 1], n >> 1) || !wait(&bars.o2read, n)) break;
             tc::tc_fence_after();
             const float *qw = slots[n % SLOTS].qw + h0;
-            const uint32_t o1 = tmem + lane_base + K::T_O + ob * 128 + h0;
+            const uint32_t o1 = tmem + lane_base + K::T_O1 + (n % K::NO1) * 64 + h0, o2 = tmem + lane_base + K::T_O2 + h0;
             float v[32];
 #pragma unroll
             for (int e = 0; e < 32; e += 16) {
                 float a[16], b[16];
-                tmem_ld16x2(o1 + e, o1 + 64 + e, a, b);
-                if (e == 16) warp_arrive(&bars.o_free[ob], lane);
+                tmem_ld16x2(o1 + e, o2 + e, a, b);
+                if (e == 16) warp_arrive(&bars.o_free[n & 1], lane);
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(qw + e + i);
@@ -671,20 +682,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int A, int B, typename TO, bool BWD>
-cudaError_t launch_t(const Maps &maps, const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out,
-                     cudaStream_t s) {
-    const int NC = (L + C - 1) / C, per = (NC + nseg - 1) / nseg;
+cudaError_t launch_t(const Maps &maps, const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out, cudaStream_t s) {
     constexpr int smem = Cfg<A, B, BWD>::SMEM;
     auto *kernel = out ? walk_tc_kernel<A, B, TO, true, BWD> : walk_tc_kernel<A, B, TO, false, BWD>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)BH * (out ? nseg : nseg - 1) * ws.n, THREADS, smem, s>>>(maps, ws, g, BH, L, nseg, per, seg_e);
     count_launches(1);
+    const dim3 grid((unsigned)BH * (out ? sg.n : sg.stretches()) * ws.n);
+    if (out && sg.n > 1) return launch_after(kernel, grid, THREADS, smem, s, maps, ws, sg, g, BH, L);
+    kernel<<<grid, THREADS, smem, s>>>(maps, ws, sg, g, BH, L);
     return cudaGetLastError();
 }
 
 template <typename TO, bool BWD>
-cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out, cudaStream_t s) {
+cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out, cudaStream_t s) {
     Maps maps;
     for (int i = 0; i < ws.n; ++i) {
         const Walk &w = ws.w[i];
@@ -693,13 +704,13 @@ cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, int nseg, float *s
             return cudaErrorInvalidValue;
     }
     const int a = ws.w[0].a, b = ws.w[0].b;
-    if (a == 128 && b == 128) return launch_t<128, 128, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
-    if (a == 128) return launch_t<128, 64, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
-    if (b == 128) return launch_t<64, 128, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
-    return launch_t<64, 64, TO, BWD>(maps, ws, g, BH, L, nseg, seg_e, out, s);
+    if (a == 128 && b == 128) return launch_t<128, 128, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
+    if (a == 128) return launch_t<128, 64, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
+    if (b == 128) return launch_t<64, 128, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
+    return launch_t<64, 64, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
 }
 
-cudaError_t launch_pass(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out_bf16, bool bwd, bool out,
+cudaError_t launch_pass(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out_bf16, bool bwd, bool out,
                         cudaStream_t s) {
     // walks of the same head sizes share a launch
     Walks part{};
@@ -707,9 +718,9 @@ cudaError_t launch_pass(const Walks &ws, Gate g, int BH, int L, int nseg, float 
     for (int i = 0; i < ws.n && e == cudaSuccess; ++i) {
         part.w[part.n++] = ws.w[i];
         if (i + 1 < ws.n && ws.w[i + 1].a == ws.w[i].a && ws.w[i + 1].b == ws.w[i].b) continue;
-        if (bwd) e = launch_ab<__nv_bfloat16, true>(part, g, BH, L, nseg, seg_e, out, s);
-        else if (out_bf16) e = launch_ab<__nv_bfloat16, false>(part, g, BH, L, nseg, seg_e, out, s);
-        else e = launch_ab<float, false>(part, g, BH, L, nseg, seg_e, out, s);
+        if (bwd) e = launch_ab<__nv_bfloat16, true>(part, g, BH, L, sg, out, s);
+        else if (out_bf16) e = launch_ab<__nv_bfloat16, false>(part, g, BH, L, sg, out, s);
+        else e = launch_ab<float, false>(part, g, BH, L, sg, out, s);
         part.n = 0;
     }
     return e;
@@ -719,27 +730,36 @@ cudaError_t launch_pass(const Walks &ws, Gate g, int BH, int L, int nseg, float 
 
 bool tc_sizes(int dk, int dv, bool bf16) { return bf16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
-int tc_segments(int BH, int L, int n) {
-    // One CTA an SM.  Cutting a sequence costs a first pass (the state update alone), so it is cut only
-    // as far as its CTAs still fit the device at once, at four chunks a segment or more.
+Segments tc_segments(int BH, int L, int n) {
+    // One CTA an SM.  Cutting a sequence costs a first pass (the state's contributions alone), so it is cut
+    // only as far as its CTAs still fit the device at once, at four chunks a segment or more; the first
+    // pass's stretches then fill the device too, at two chunks each or more.
     const long long units = (long long)BH * n;
     const int NC = (L + C - 1) / C;
+    Segments sg{};
+    sg.chunks = NC;
     long long want = 148 / units;
     if (want > NC / 4) want = NC / 4;
-    if (want < 2) return 1;
-    const int per = (int)((NC + want - 1) / want);
-    return (NC + per - 1) / per;
+    if (want < 2) return sg;
+    int per = (int)((NC + want - 1) / want), m = (NC + per - 1) / per;
+    long long fine = 148 / (units * (m - 1));
+    if (fine > per / 2) fine = per / 2;
+    if (fine < 1) fine = 1;
+    sg.fine = (int)fine;
+    sg.chunks = (per + sg.fine - 1) / sg.fine * sg.fine;
+    sg.n = (NC + sg.chunks - 1) / sg.chunks;
+    return sg;
 }
 
-cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, int nseg, float *seg_e, bool out_bf16, bool bwd,
+cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out_bf16, bool bwd,
                             cudaStream_t s) {
     cudaError_t e = cudaSuccess;
-    if (nseg > 1) {
-        e = launch_pass(ws, g, BH, L, nseg, seg_e, out_bf16, bwd, false, s);
-        if (e == cudaSuccess) e = launch_seg_chain(ws, seg_e, BH, nseg, s);
+    if (sg.n > 1) {
+        e = launch_pass(ws, g, BH, L, sg, out_bf16, bwd, false, s);
+        if (e == cudaSuccess) e = launch_seg_chain(ws, sg, BH, s);
         if (e != cudaSuccess) return e;
     }
-    return launch_pass(ws, g, BH, L, nseg, seg_e, out_bf16, bwd, true, s);
+    return launch_pass(ws, g, BH, L, sg, out_bf16, bwd, true, s);
 }
 
 cudaError_t read_and_clear_error(unsigned int *out) {
