@@ -68,7 +68,7 @@ struct Walks {
 };
 
 constexpr int C = 64;             // tokens in a chunk
-constexpr float L_MIN = -200.f;   // e^L_MIN is 0 in fp32: lower log-decays (-inf) act as this one
+constexpr float L_MIN = -200.f;   // e^L_MIN is 0 in fp32: lower log-decays (-inf) act as this one (above, 200 does)
 
 // CUDA-core walks: any a, b <= 128, fp32 arithmetic; blocks of SIMT_BT value columns.
 constexpr int SIMT_BT = 32;

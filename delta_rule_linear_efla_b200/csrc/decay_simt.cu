@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(NT, 2)
         if (sin && i < a && j < nb) v = st ? sin[(size_t)(j0 + j) * a + i] : sin[(size_t)i * b + j0 + j];
         S[i * ZP + j] = v;
     }
-    Sum seg_sum{0.f, 0.f};
+    Fixed seg_sum = 0;
+    bool seg_good = true;
 
     const int r4 = (tid >> 4) * 4, tc = tid & 15;  // P: rows r4.., columns tc + 16 j; out: columns 2 tc, 2 tc + 1
     for (int it = i0; it < i1; ++it) {
@@ -127,17 +128,20 @@ __global__ void __launch_bounds__(NT, 2)
         if (warp == 0) {
             const int t = t0 + 2 * lane;
             const PairSum c = chunk_sums(gate_or_zero(g, bh, L, t), gate_or_zero(g, bh, L, t + 1), lane);
-            const Sum cC = last_sum(c), cc[2] = {c.c0, c.c1};
+            const Fixed cc[2] = {c.c0, c.c1};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float up = exp2_sum(cc[e]), down = exp2_sum(cC - cc[e]);
-                qw[2 * lane + e] = rev ? down : up;
-                kw[2 * lane + e] = rev ? up : down;
-                chi[2 * lane + e] = cc[e].hi;
-                clo[2 * lane + e] = cc[e].lo;
+                const int t = 2 * lane + e;
+                const float up = if_good(exp2_fixed(cc[e]), t < c.bad), down = if_good(exp2_fixed(c.cC - cc[e]), c.bad == C || t >= c.bad);
+                qw[t] = rev ? down : up;
+                kw[t] = rev ? up : down;
+                const float hi = __ll2float_rn(cc[e]);
+                chi[t] = if_good(hi * (1.f / FIXED_ONE), t < c.bad);
+                clo[t] = __ll2float_rn(cc[e] - __float2ll_rn(hi)) * (1.f / FIXED_ONE);
             }
-            if (lane == 0) tot[0] = exp2_sum(cC);
-            seg_sum = seg_sum + cC;
+            if (lane == 0) tot[0] = if_good(exp2_fixed(c.cC), c.bad == C);
+            seg_sum = max(seg_sum + c.cC, FIXED_MIN);
+            seg_good = seg_good && c.bad == C;
         }
         __syncthreads();
         if (OUT) {
@@ -270,7 +274,7 @@ __global__ void __launch_bounds__(NT, 2)
     }
     // every walk in the same direction finds the same decay of a segment: its first one writes it
     if (!OUT && warp == 0 && lane == 0 && blk == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
-        sg.e[((size_t)(rev ? 1 : 0) * BH + bh) * (sg.n - 1) + seg] = exp2_sum(seg_sum);
+        sg.e[((size_t)(rev ? 1 : 0) * BH + bh) * (sg.n - 1) + seg] = if_good(exp2_fixed(seg_sum), seg_good);
 }
 
 template <typename T, typename TO>

@@ -18,7 +18,9 @@
 //           a suffix sum of q.dq - k.dk that cancels down to the pairs that straddle a token; errors of
 //           D o P cancel with them (dq and dk round the same products), errors of two different state
 //           copies would not, and would grow with the square root of the sequence.
-// Decay factors and the sums over them are fp32 (their logarithms' sums two fp32 each, decay_gate.cuh).
+// Decay factors and the sums over them are fp32; their logarithms' sums are integers (decay_gate.cuh), rounded
+// to fp32 for the factors within a chunk alone, which is at most 2^-10 of a factor where a chunk forgets
+// everything at every token (sums of 18000), and 2^-15 with one such token: below the rounding of D o P.
 //
 // Warp roles (one CTA an SM, 24 warps):
 //   0-3   weight:  Yw's halves from Y's tile
@@ -49,7 +51,7 @@ namespace {
 constexpr int WARPS = 24, THREADS = WARPS * 32;
 constexpr int W_STATE = 20, W_INTRA = 21, W_TMA = 22, W_GATE = 23;
 constexpr int NS = 3;     // stages of X, Y, Z
-constexpr int SLOTS = 4;  // chunks of decay weights
+constexpr int GB = 4, SLOTS = 2 * GB;  // chunks whose decay weights are made at once, and kept
 constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
 
 struct Maps {
@@ -73,20 +75,20 @@ struct Cfg {
 
 struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
-    uint64_t full[NS], gready[SLOTS], y_free[2], pdone[2], d1done, d2done, o1done[2], o2done, o2read, drain[2];
+    uint64_t full[NS], gready[2], y_free[2], pdone[2], d1done, d2done, o1done[2], o2done, o2read, drain[2];
     // one arrival from each of four warps
     uint64_t p_ready, s_ready;
-    uint64_t gfree[SLOTS], o_free[2];  // the eight output warps (without output, gfree: the weights' sixteen)
+    uint64_t gfree[2], o_free[2];  // the eight output warps (without output, gfree: the weights' sixteen)
     uint64_t y_ready[2];               // the weights' four warps, sixteen without output
     uint64_t free_s[NS];               // one from each issuer
 };
-constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + SLOTS + 2 + 2 + 2 + 2 + 2 + 2, BARS_FOUR = BARS_ONE + 2,
-              BARS_OUT = BARS_FOUR + SLOTS + 2, BARS_Y = BARS_OUT + 2;
+constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 2 + 2 + 2 + 2, BARS_FOUR = BARS_ONE + 2,
+              BARS_OUT = BARS_FOUR + 2 + 2, BARS_Y = BARS_OUT + 2;
 
 struct Slot {
     float qw[C], kw[C];
-    float gw[C];   // 2^(c_end - c) within a token's group of eight (end: its last token in walking order)
-    float2 c2[C];  // running sum in units of log 2 (its negative backwards), hi and lo
+    float gw[C];  // 2^(c_end - c) within a token's group of eight (end: its last token in walking order)
+    float c2[C];  // running sum in units of log 2 (its negative backwards)
     float tot, pad[3];
 };
 
@@ -182,6 +184,8 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+__device__ __forceinline__ float ex2_fixed(Fixed x) { return ex2(__ll2float_rn(x) * (1.f / FIXED_ONE)); }
 
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = tmem_base, lane_base = (uint32_t)(32 * (warp & 3)) << 16, sb = tc::smem_u32(base);
     const long long budget = WAIT_BUDGET;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity & 1, &abort_flag); };
-    auto wait_gate = [&](int n) { return wait(&bars.gready[n % SLOTS], n / SLOTS); };
+    auto wait_gate = [&](int n) { return n % GB != 0 || wait(&bars.gready[n / GB & 1], n / SLOTS); };
 
     if (warp == W_TMA) {
         const bool leader = elect();
@@ -414,41 +418,69 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         tc::mbar_wait(&bars.drain[1], 0, budget / 4);
     } else if (warp == W_GATE) {
-        Sum sum{0.f, 0.f};
-        int t = chunk(0) * C + 2 * lane;
-        float l0 = gate_or_zero(g, bh, L, t), l1 = gate_or_zero(g, bh, L, t + 1);
-        for (int n = 0; n < cnt; ++n) {
-            const PairSum c = chunk_sums(l0, l1, lane);
-            const Sum cC = last_sum(c), cc[2] = {c.c0, c.c1};
-            const float after = OUT ? 1.f : exp2_sum(sum);  // the decay of the chunks already walked
-            sum = sum + cC;
-            if (n + 1 < cnt) {  // the next chunk's, while this one's weights are made
-                t = chunk(n + 1) * C + 2 * lane;
-                l0 = gate_or_zero(g, bh, L, t);
-                l1 = gate_or_zero(g, bh, L, t + 1);
-            }
-            if (n >= SLOTS && !wait(&bars.gfree[n % SLOTS], n / SLOTS - 1)) break;
-            Slot &sl = slots[n % SLOTS];
+        // Four chunks at once: eight lanes a chunk, eight tokens a lane (one chunk at a time, in pairs of tokens,
+        // took 3000 cycles a chunk: a long dependent stretch of code that runs once).
+        Fixed sum = 0;
+        bool good = true;
+        float l[8];
+        const int gk = lane >> 3, tk = 8 * (lane & 7);  // this lane's chunk of the four, and its first token in it
+        auto load = [&](int n) {
+            const int t = n + gk < cnt ? chunk(n + gk) * C + tk : L;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float up = exp2_sum(cc[e]), down = exp2_sum(cC - cc[e]);
-                sl.qw[2 * lane + e] = rev ? down : up;
-                sl.kw[2 * lane + e] = (rev ? up : down) * (OUT ? 1.f : after);
-                const Sum x = rev ? Sum{-cc[e].hi, -cc[e].lo} : cc[e];
-                sl.c2[2 * lane + e] = make_float2(x.hi, x.lo);
-                // the group is four lanes
-                const int src = rev ? lane & ~3 : lane | 3;
-                const Sum end = rev ? c.c0 : c.c1;
-                const Sum ce = {__shfl_sync(0xffffffffu, end.hi, src), __shfl_sync(0xffffffffu, end.lo, src)};
-                sl.gw[2 * lane + e] = exp2_sum(rev ? cc[e] - ce : ce - cc[e]);
+            for (int i = 0; i < 8; ++i) l[i] = gate_or_zero(g, bh, L, t + i);
+        };
+        load(0);
+        for (int n = 0; n < cnt; n += GB) {
+            Fixed c[8];
+            int bad = C;  // the first token of the chunk whose log-decay is not a number: later sums are not either
+#pragma unroll
+            for (int i = 7; i >= 0; --i) {
+                c[i] = to_fixed(l[i]);
+                if (l[i] != l[i]) bad = tk + i;
             }
-            if (lane == 0) sl.tot = exp2_sum(cC);
+            if (n + GB < cnt) load(n + GB);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) c[i] += c[i - 1];
+            Fixed s = c[7];
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const Fixed y = __shfl_up_sync(0xffffffffu, s, o, 8);
+                if ((lane & 7) >= o) s += y;
+                bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, o));
+            }
+            const Fixed before = s - c[7], cC = __shfl_sync(0xffffffffu, s, 7, 8);
+            float after = 1.f;
+            if (!OUT) {  // the decay of the chunks already walked, the batch's earlier ones among them
+#pragma unroll
+                for (int k = 0; k < GB; ++k) {
+                    if (k == gk) after = if_good(exp2_fixed(sum), good);
+                    sum = max(sum + __shfl_sync(0xffffffffu, cC, 8 * k), FIXED_MIN);
+                    good = good && __shfl_sync(0xffffffffu, bad, 8 * k) == C;
+                }
+            }
+            const int bi = n / GB & 1;
+            if (n >= SLOTS && !wait(&bars.gfree[bi], n / SLOTS - 1)) break;
+            Slot &sl = slots[bi * GB + gk];
+            const Fixed ce = before + (rev ? c[0] : c[7]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const Fixed x = before + c[i];
+                const float up = if_good(ex2_fixed(x), tk + i < bad), down = if_good(ex2_fixed(cC - x), bad == C || tk + i >= bad);
+                sl.kw[tk + i] = (rev ? up : down) * after;
+                if (OUT) {
+                    sl.qw[tk + i] = rev ? down : up;
+                    sl.gw[tk + i] = ex2_fixed(rev ? x - ce : ce - x);
+                    const float h = __ll2float_rn(x) * (1.f / FIXED_ONE);
+                    sl.c2[tk + i] = if_good(rev ? -h : h, tk + i < bad);
+                }
+            }
+            if (OUT && (lane & 7) == 0) sl.tot = if_good(ex2_fixed(cC), bad == C);
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars.gready[n % SLOTS]);
+            if (lane == 0) tc::mbar_arrive(&bars.gready[bi]);
         }
         // every walk in the same direction finds the same decay of a segment: its first one writes it
         if (!OUT && lane == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
-            sg.e[((size_t)(rev ? 1 : 0) * BH + bh) * segs + seg] = exp2_sum(sum);
+            sg.e[((size_t)(rev ? 1 : 0) * BH + bh) * segs + seg] = if_good(exp2_fixed(sum), good);
     } else if (OUT ? wg == 0 : wg < 4) {
         // ---------------------------------------------------------- Yw
         for (int n = 0; n < cnt; ++n) {
@@ -472,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             tc::fence_async_smem();
             warp_arrive(&bars.y_ready[n & 1], lane);
-            if (!OUT && lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
+            if (!OUT && lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
         }
         if (!OUT && wg == 0 && wait(&bars.drain[0], 0)) {  // the segment's contribution
             const int j = acc_row<B>(warp, lane);
@@ -505,51 +537,54 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!wait_gate(n) || !wait(&bars.pdone[n & 1], n >> 1)) break;
             tc::tc_fence_after();
             const Slot &sl = slots[n % SLOTS];
-            const float2 ca = sl.c2[r], cb = sl.c2[r + 8];
+            const float ca = sl.c2[r], cb = sl.c2[r + 8];
             const uint32_t tp = tmem + lane_base + K::T_P + (n & 1) * 64;
-            uint32_t u[4];
+            uint32_t u[4][4];  // the diagonal block, and up to three on the on side
             {
                 float v[8];
                 tmem_ld_16x256(tp + r0, v);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int c = r0 + 8 * k + cq;
-                    const float4 cc = *reinterpret_cast<const float4 *>(&sl.c2[c]);
+                    const float2 cc = *reinterpret_cast<const float2 *>(&sl.c2[c]);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {  // row r + 8 e, columns c and c + 1
-                        const float2 cr = e ? cb : ca;
+                        const float cr = e ? cb : ca;
                         const int a = rev ? c - r - 8 * e : r + 8 * e - c, a1 = rev ? a + 1 : a - 1;  // on where >= 0
-                        const float x0 = (cr.x - cc.x) + (cr.y - cc.y), x1 = (cr.x - cc.z) + (cr.y - cc.w);
-                        u[2 * k + e] = tc::pack_bf16(a >= 0 ? v[4 * k + 2 * e] * ex2(x0) : 0.f,
-                                                     a1 >= 0 ? v[4 * k + 2 * e + 1] * ex2(x1) : 0.f);
+                        u[3][2 * k + e] = tc::pack_bf16(a >= 0 ? v[4 * k + 2 * e] * ex2(cr - cc.x) : 0.f,
+                                                        a1 >= 0 ? v[4 * k + 2 * e + 1] * ex2(cr - cc.y) : 0.f);
+                    }
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < 3; ++b) {
+                const int c0 = on0 + 16 * b;
+                if (c0 < on1) {
+                    float v[8];
+                    tmem_ld_16x256(tp + c0, v);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float ce = sl.c2[c0 + 8 * k + (rev ? 0 : 7)];
+                        const F2 f = *reinterpret_cast<const F2 *>(&sl.gw[c0 + 8 * k + cq]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = ex2((e ? cb : ca) - ce);
+                            u[b][2 * k + e] = pack(f2(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]) * (f2(x, x) * f));
+                        }
                     }
                 }
             }
             if (n > 0 && !wait(&bars.o2done, n - 1)) break;  // the tile's last reader
-            auto store = [&](int c0) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+            for (int b = 0; b < 4; ++b) {
+                const int c0 = b == 3 ? r0 : on0 + 16 * b;
+                if (b == 3 || c0 < on1) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<uint32_t *>(pt + tc::sw128_off(r + 8 * e, (c0 >> 3) + k) + 2 * cq) = u[2 * k + e];
-            };
-            store(r0);
-#pragma unroll 1
-            for (int c0 = on0; c0 < on1; c0 += 16) {
-                float v[8];
-                tmem_ld_16x256(tp + c0, v);
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float2 ce = sl.c2[c0 + 8 * k + (rev ? 0 : 7)];
-                    const F2 f = *reinterpret_cast<const F2 *>(&sl.gw[c0 + 8 * k + cq]);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float2 cr = e ? cb : ca;
-                        const float x = ex2((cr.x - ce.x) + (cr.y - ce.y));
-                        u[2 * k + e] = pack(f2(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]) * (f2(x, x) * f));
-                    }
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<uint32_t *>(pt + tc::sw128_off(r + 8 * e, (c0 >> 3) + k) + 2 * cq) = u[b][2 * k + e];
                 }
-                store(c0);
             }
             tc::fence_async_smem();
             warp_arrive(&bars.p_ready, lane);
@@ -652,7 +687,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars.gfree[n % SLOTS]);
+            if (lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
             if (j >= 0) {
                 TO *out = static_cast<TO *>(w.out) + row0 * B + j;
                 if (cl == 32) {
