@@ -35,20 +35,8 @@ struct Gate {
     int H;
 };
 
-// A long sequence with few heads is cut into n segments, walked at the same time: a first pass gives the
-// stretches' own contributions to the state (u) and their whole decays (e), a second kernel chains them to
-// the states that enter the segments (in), and the walk proper follows.  fine: stretches of the first pass
-// in a segment (it has one segment less to do, and much less to do in it).
-struct Segments {
-    int n = 1, fine = 1;
-    int chunks;        // chunks in a segment, a multiple of fine
-    float *e;          // [2][BH][(n - 1) fine]: forward walks, backward walks
-    int stretches() const { return (n - 1) * fine; }
-};
-
-// One walk.  u, in: [BH][(n - 1) fine][a][b] and [BH][n][a][b] fp32, in walking order (unused with one
-// segment).  dotx / dot: where dot is given, each token's dotx_t . out_t before out is
-// rounded, as shares of the column blocks ([blocks][BH][L] fp32, added by the gradient kernel).
+// One walk.  dotx / dot: where dot is given, each token's dotx_t . out_t before out is rounded, as shares
+// ([planes][BH][L] fp32, added by the gradient kernel).
 struct Walk {
     const void *x, *y, *z;
     const float *s0;  // the state that enters, or null for zero
@@ -58,7 +46,6 @@ struct Walk {
     int a, b, rev;
     const void *dotx;
     float *dot;
-    float *u, *in;
 };
 
 constexpr int MAX_WALKS = 3;
@@ -70,24 +57,42 @@ struct Walks {
 constexpr int C = 64;             // tokens in a chunk
 constexpr float L_MIN = -200.f;   // e^L_MIN is 0 in fp32: lower log-decays (-inf) act as this one (above, 200 does)
 
-// CUDA-core walks: any a, b <= 128, fp32 arithmetic; blocks of SIMT_BT value columns.
+// Where whole walks would leave processors idle (few heads, or a last round with few of them), sequences are
+// cut: a first pass gives every stretch's own contribution to the state (u, fp32 [a][b]) and its whole decay
+// (e), both for every stretch that does not end its sequence, and the walk proper starts a stretch from
+// S = e_i S + u_i over the stretches before it.
+
+// CUDA-core walks: any a, b <= 128, fp32 arithmetic; blocks of SIMT_BT value columns.  Every sequence is cut
+// into n segments of `chunks` chunks.
 constexpr int SIMT_BT = 32;
+struct Segments {
+    int n, chunks;
+    float *u[MAX_WALKS];  // [BH][n - 1][a][b]
+    float *e;             // [2][BH][n - 1]: forward walks, backward walks
+};
 Segments simt_segments(int BH, int L, const int *blocks, int n);
 cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool in_bf16, bool out_bf16,
                               cudaStream_t s);
 
 // Tensor-core walks (decay_tc.cu): bf16 inputs, a and b of 64 or 128, x, y and z 16-byte aligned.  bwd: walks
 // with dots, given as DOT_PLANES shares (one for each warp of the output group); outputs are bf16.
+// All walks (of the same head sizes) one after another, head by head, are one row of chunks, and each of g CTAs
+// takes an even share of it: the end of one walk, whole ones, the start of another.  The stretch of a share
+// that does not end its sequence is the last one; the first pass takes it in `fine` parts.
 constexpr int DOT_PLANES = 4;
+struct Shares {
+    int g, fine;
+    long long size;  // chunks in a share; the first `more` have one more
+    int more;
+    float *u;  // [(g - 1) fine][a][b]
+    float *e;  // [(g - 1) fine]
+    int stretches() const { return fine > 0 ? (g - 1) * fine : 0; }  // fine = 0: shares are whole walks
+};
 bool tc_sizes(int dk, int dv, bool in_bf16);
-Segments tc_segments(int BH, int L, int n);
-cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out_bf16, bool bwd,
+Shares tc_shares(int BH, int L, int n);
+cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, const Shares &sh, bool out_bf16, bool bwd,
                             cudaStream_t s);
 cudaError_t read_and_clear_error(unsigned int *out);
-
-// The states that enter the segments: S_0 the state that enters the walk, S_{i+1} = e_i S_i + u_i over the
-// stretches.
-cudaError_t launch_seg_chain(const Walks &ws, const Segments &sg, int BH, cudaStream_t s);
 
 // dl from the walks' dots: dotq [nq][BH][L], dotk [nk][BH][L] (shares of their column blocks);
 // dS_final [BH][dk][dv] and the forward walk's end state S_end [BH][dv][dk], or both null.

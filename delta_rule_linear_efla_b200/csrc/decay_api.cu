@@ -10,6 +10,7 @@ namespace {
 
 using efla::decay::Gate;
 using efla::decay::Segments;
+using efla::decay::Shares;
 using efla::decay::Walk;
 using efla::decay::Walks;
 
@@ -42,39 +43,50 @@ struct Arena {
 
 int blocks_of(int b) { return (b + efla::decay::SIMT_BT - 1) / efla::decay::SIMT_BT; }
 
-// The walks' segments and their states: lays them out in the arena.
-Segments plan_segments(Walks &ws, int BH, int L, bool tc, Arena &ar) {
+// How CUDA-core walks are cut, and their stretches' contributions.
+Segments plan_segments(const Walks &ws, int BH, int L, Arena &ar) {
     int blocks[efla::decay::MAX_WALKS];
     for (int i = 0; i < ws.n; ++i) blocks[i] = blocks_of(ws.w[i].b);
-    Segments sg = tc ? efla::decay::tc_segments(BH, L, ws.n) : efla::decay::simt_segments(BH, L, blocks, ws.n);
+    Segments sg = efla::decay::simt_segments(BH, L, blocks, ws.n);
     if (sg.n > 1) {
-        for (int i = 0; i < ws.n; ++i) {
-            const size_t ab = (size_t)ws.w[i].a * ws.w[i].b;
-            ws.w[i].u = ar.floats(BH * sg.stretches() * ab);
-            ws.w[i].in = ar.floats(BH * sg.n * ab);
-        }
-        sg.e = ar.floats((size_t)2 * BH * sg.stretches());
+        for (int i = 0; i < ws.n; ++i) sg.u[i] = ar.floats((size_t)BH * (sg.n - 1) * ws.w[i].a * ws.w[i].b);
+        sg.e = ar.floats((size_t)2 * BH * (sg.n - 1));
     }
     return sg;
 }
 
+// The same of tensor-core walks of the same head sizes.
+Shares plan_shares(const Walks &ws, int BH, int L, Arena &ar) {
+    Shares sh = efla::decay::tc_shares(BH, L, ws.n);
+    if (const int n = sh.stretches()) {
+        sh.u = ar.floats((size_t)n * ws.w[0].a * ws.w[0].b);
+        sh.e = ar.floats(n);
+    }
+    return sh;
+}
+
 struct FwdPlan {
     Walks ws{};
-    Segments sg;
+    Segments sg{};
+    Shares sh{};
     size_t bytes = 0;
     FwdPlan(int BH, int L, int dk, int dv, bool tc, void *base) {
         Arena ar{static_cast<char *>(base)};
         ws.n = 1;
         ws.w[0].a = dk;
         ws.w[0].b = dv;
-        sg = plan_segments(ws, BH, L, tc, ar);
+        if (tc) sh = plan_shares(ws, BH, L, ar);
+        else sg = plan_segments(ws, BH, L, ar);
         bytes = ar.used;
     }
 };
 
 struct BwdPlan {
-    Walks ws{};  // dq, dk, dv
-    Segments sg;
+    Walks ws{};              // dq, dk, dv
+    Walks part[2]{};         // tensor-core launches: those of the same head sizes together
+    int parts = 0;
+    Segments sg{};
+    Shares sh[2]{};
     float *S_end = nullptr, *dotq = nullptr, *dotk = nullptr;
     int planes = 1;
     size_t bytes = 0;
@@ -88,8 +100,22 @@ struct BwdPlan {
         dotq = ar.floats((size_t)planes * BH * L);
         dotk = ar.floats((size_t)planes * BH * L);
         S_end = ar.floats((size_t)BH * dk * dv);
-        sg = plan_segments(ws, BH, L, tc, ar);
+        if (!tc) {
+            sg = plan_segments(ws, BH, L, ar);
+        } else {
+            parts = dk == dv ? 1 : 2;
+            split();
+            for (int i = 0; i < parts; ++i) sh[i] = plan_shares(part[i], BH, L, ar);
+        }
         bytes = ar.used;
+    }
+    // The launches' walks, from ws as it is now.
+    void split() {
+        part[0] = part[1] = Walks{};
+        for (int i = 0; i < 3; ++i) {
+            Walks &p = part[parts == 2 && i == 2 ? 1 : 0];
+            p.w[p.n++] = ws.w[i];
+        }
     }
 };
 
@@ -141,7 +167,7 @@ efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, co
     w.out = o;
     w.s_end = S_final;
     const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
-    if (tc) return from_cuda(efla::decay::launch_walks_tc(p.ws, g, BH, L, p.sg, o_dt == EFLA_BF16, false, s));
+    if (tc) return from_cuda(efla::decay::launch_walks_tc(p.ws, g, BH, L, p.sh, o_dt == EFLA_BF16, false, s));
     return from_cuda(efla::decay::launch_walks_simt(p.ws, g, BH, L, p.sg, dt == EFLA_BF16,
                                                     o_dt == EFLA_BF16, s));
 }
@@ -197,8 +223,14 @@ efla_status efla_decay_bwd(const void *q, const void *k, const void *v, const vo
     }
     const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};
     const bool bf16 = dt == EFLA_BF16;
-    const cudaError_t e = tc ? efla::decay::launch_walks_tc(p.ws, g, BH, L, p.sg, bf16, true, s)
-                             : efla::decay::launch_walks_simt(p.ws, g, BH, L, p.sg, bf16, bf16, s);
+    cudaError_t e = cudaSuccess;
+    if (tc) {
+        p.split();
+        for (int i = 0; i < p.parts && e == cudaSuccess; ++i)
+            e = efla::decay::launch_walks_tc(p.part[i], g, BH, L, p.sh[i], bf16, true, s);
+    } else {
+        e = efla::decay::launch_walks_simt(p.ws, g, BH, L, p.sg, bf16, bf16, s);
+    }
     if (e != cudaSuccess || !want_dl) return from_cuda(e);
     return from_cuda(efla::decay::launch_dlog(p.dotq, p.planes, p.dotk, p.planes, dS_final, tail ? p.S_end : nullptr, g, dlog_g,
                                               BH, L, dk, dv, s));

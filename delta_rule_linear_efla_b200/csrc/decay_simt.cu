@@ -104,13 +104,15 @@ __global__ void __launch_bounds__(NT, 2)
 
     // ---- the state that enters
     const size_t sbh = (size_t)bh * a * b;
-    const float *sin = nullptr;
-    if (OUT) sin = sg.n > 1 ? w.in + ((size_t)bh * sg.n + seg) * a * b : (w.s0 ? w.s0 + sbh : nullptr);
-    const bool st = sg.n == 1 && w.s0_t;
+    const float *s0 = OUT && w.s0 ? w.s0 + sbh : nullptr;
+    const float *eb = sg.e + ((size_t)(rev ? 1 : 0) * BH + bh) * (sg.n - 1), *ub = sg.u[wi] + (size_t)bh * (sg.n - 1) * a * b;
     for (int e = tid; e < ap * BT; e += NT) {
         const int i = e / BT, j = e % BT;
         float v = 0.f;
-        if (sin && i < a && j < nb) v = st ? sin[(size_t)(j0 + j) * a + i] : sin[(size_t)i * b + j0 + j];
+        if (OUT && i < a && j < nb) {
+            if (s0) v = w.s0_t ? s0[(size_t)(j0 + j) * a + i] : s0[(size_t)i * b + j0 + j];
+            for (int k = 0; k < seg; ++k) v = fmaf(eb[k], v, ub[(size_t)k * a * b + (size_t)i * b + j0 + j]);
+        }
         S[i * ZP + j] = v;
     }
     Fixed seg_sum = 0;
@@ -264,7 +266,7 @@ __global__ void __launch_bounds__(NT, 2)
     }
     __syncthreads();
     float *sout = nullptr;
-    if (!OUT) sout = w.u + ((size_t)bh * (sg.n - 1) + seg) * a * b;
+    if (!OUT) sout = sg.u[wi] + ((size_t)bh * (sg.n - 1) + seg) * a * b;
     else if (seg == sg.n - 1 && w.s_end) sout = w.s_end + sbh;
     if (sout) {
         for (int e = tid; e < a * BT; e += NT) {
@@ -298,57 +300,9 @@ cudaError_t launch_t(const Walks &ws, Gate g, int BH, int L, const Segments &sg,
     part<<<dim3(blocks * BH, sg.n - 1), NT, smem, s>>>(ws, sg, g, BH, L);
     count_launches(1);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_seg_chain(ws, sg, BH, s);
     if (e != cudaSuccess) return e;
     count_launches(1);
     return launch_after(full, dim3(blocks * BH, sg.n), NT, smem, s, ws, sg, g, BH, L);
-}
-
-// One thread per VEC state elements.
-template <int VEC>
-__global__ void __launch_bounds__(128)
-    seg_chain_kernel(const __grid_constant__ Walks ws, const __grid_constant__ Segments sg, int BH) {
-    cudaGridDependencySynchronize();
-    const Walk &w = ws.w[blockIdx.z];
-    const int ab = w.a * w.b, bh = blockIdx.x, e0 = (blockIdx.y * 128 + threadIdx.x) * VEC, nf = (sg.n - 1) * sg.fine;
-    if (e0 >= ab) return;
-    const float *ee = sg.e + ((size_t)(w.rev ? 1 : 0) * BH + bh) * nf;
-    const float *u = w.u + (size_t)bh * nf * ab + e0;
-    float *in = w.in + (size_t)bh * sg.n * ab + e0;
-    float s[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const int x = (e0 + i) / w.b, y = (e0 + i) - x * w.b;
-        s[i] = w.s0 ? w.s0[(size_t)bh * ab + (w.s0_t ? y * w.a + x : e0 + i)] : 0.f;
-    }
-    auto store = [&](int k) {
-        if constexpr (VEC == 4) *reinterpret_cast<float4 *>(in + (size_t)k * ab) = make_float4(s[0], s[1], s[2], s[3]);
-        else in[(size_t)k * ab] = s[0];
-    };
-    store(0);
-    constexpr int AHEAD = 4;
-    for (int f0 = 0; f0 < nf; f0 += AHEAD) {
-        float v[AHEAD][VEC], f[AHEAD];
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (f0 + k < nf) {
-                f[k] = ee[f0 + k];
-                const float *p = u + (size_t)(f0 + k) * ab;
-                if constexpr (VEC == 4) {
-                    const float4 t = *reinterpret_cast<const float4 *>(p);
-                    v[k][0] = t.x; v[k][1] = t.y; v[k][2] = t.z; v[k][3] = t.w;
-                } else {
-                    v[k][0] = *p;
-                }
-            }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (f0 + k < nf) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) s[i] = fmaf(f[k], s[i], v[k][i]);
-                if ((f0 + k + 1) % sg.fine == 0) store((f0 + k + 1) / sg.fine);
-            }
-    }
 }
 
 constexpr int DL_T = 512, DL_E = 8;
@@ -429,6 +383,7 @@ Segments simt_segments(int BH, int L, const int *blocks, int n) {
     long long ctas = 0;
     for (int i = 0; i < n; ++i) ctas += (long long)blocks[i] * BH;
     const int NC = (L + C - 1) / C;
+    sg.n = 1;
     sg.chunks = NC;
     if (ctas >= 148) return sg;
     long long want = (2 * 148 + ctas - 1) / ctas;
@@ -437,19 +392,6 @@ Segments simt_segments(int BH, int L, const int *blocks, int n) {
     sg.chunks = (int)((NC + want - 1) / want);
     sg.n = (NC + sg.chunks - 1) / sg.chunks;
     return sg;
-}
-
-cudaError_t launch_seg_chain(const Walks &ws, const Segments &sg, int BH, cudaStream_t s) {
-    int ab = 1;
-    bool vec = true;
-    for (int i = 0; i < ws.n; ++i) {
-        const int n = ws.w[i].a * ws.w[i].b;
-        ab = n > ab ? n : ab;
-        vec = vec && n % 4 == 0;
-    }
-    count_launches(1);
-    if (vec) return launch_after(seg_chain_kernel<4>, dim3(BH, (ab + 511) / 512, ws.n), 128, 0, s, ws, sg, BH);
-    return launch_after(seg_chain_kernel<1>, dim3(BH, (ab + 127) / 128, ws.n), 128, 0, s, ws, sg, BH);
 }
 
 cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool in_bf16, bool out_bf16,

@@ -18,9 +18,9 @@
 //           a suffix sum of q.dq - k.dk that cancels down to the pairs that straddle a token; errors of
 //           D o P cancel with them (dq and dk round the same products), errors of two different state
 //           copies would not, and would grow with the square root of the sequence.
-// Decay factors and the sums over them are fp32; their logarithms' sums are integers (decay_gate.cuh), rounded
-// to fp32 for the factors within a chunk alone, which is at most 2^-10 of a factor where a chunk forgets
-// everything at every token (sums of 18000), and 2^-15 with one such token: below the rounding of D o P.
+// Decay factors and the sums of their logarithms are fp32.  The factors within a chunk take differences of
+// running sums, off by at most 2^-10 where a chunk forgets everything at every token (sums of 18000) and 2^-15
+// with one such token: below the rounding of D o P.
 //
 // Warp roles (one CTA an SM, 24 warps):
 //   0-3   weight:  Yw's halves from Y's tile
@@ -107,27 +107,31 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
 // Bounded wait that also gives up once another role has.  The try_wait carries a suspend-time hint (as a
 // kernel of 19 warps that mostly wait must): without one the waiting warps' polls took four of five issue
 // slots from the working ones (a chunk took 8800 cycles).
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
-    const uint32_t addr = tc::smem_u32(bar);
-    long long t0 = 0;
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(addr), "r"(parity), "r"(1000000u)
-            : "memory");
-        if (ok) return true;
+__device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool wait_longer(uint32_t addr, uint32_t parity, volatile int *abort_flag) {
+    const long long t0 = clock64();
+    while (!try_wait(addr, parity)) {
         if (*abort_flag) return false;
-        const long long t = clock64();
-        if (t0 == 0) t0 = t;
-        if (t - t0 > WAIT_BUDGET) {
+        if (clock64() - t0 > WAIT_BUDGET) {
             *abort_flag = 1;
             return false;
         }
     }
+    return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
+    const uint32_t addr = tc::smem_u32(bar);
+    return try_wait(addr, parity) || wait_longer(addr, parity, abort_flag);
 }
 
 // 16 lanes x 16 columns of tensor memory, a row of eight columns on four threads: v[4 k + 2 e + i] is row
@@ -185,8 +189,6 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ float ex2_fixed(Fixed x) { return ex2(__ll2float_rn(x) * (1.f / FIXED_ONE)); }
-
 __device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
@@ -239,21 +241,22 @@ __device__ __forceinline__ float column_sums(float (&p)[32], int lane) {
     return p[0];
 }
 
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void put2(float *p, float *q, float x, float y) { *p = x; *q = y; }
-__device__ __forceinline__ void put2(__nv_bfloat16 *p, __nv_bfloat16 *q, float x, float y) {
+__device__ __forceinline__ void put2(float *p, float *q, float x, float y, bool on_p, bool on_q) {
+    if (on_p) *p = x;
+    if (on_q) *q = y;
+}
+__device__ __forceinline__ void put2(__nv_bfloat16 *p, __nv_bfloat16 *q, float x, float y, bool on_p, bool on_q) {
     const uint32_t u = tc::pack_bf16(x, y);
-    *reinterpret_cast<unsigned short *>(p) = (unsigned short)u;
-    *reinterpret_cast<unsigned short *>(q) = (unsigned short)(u >> 16);
+    if (on_p) *reinterpret_cast<unsigned short *>(p) = (unsigned short)u;
+    if (on_q) *reinterpret_cast<unsigned short *>(q) = (unsigned short)(u >> 16);
 }
 
 // OUT = false: the stretch's own contribution to the state only (the segments' first pass).  BWD: walks
 // that may have dots (w.dot), with the state's copy in two halves where they do.
 template <int A, int B, typename TO, bool OUT, bool BWD>
 __global__ void __launch_bounds__(THREADS, 1)
-    walk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Walks ws, const __grid_constant__ Segments sg,
-                   const Gate g, int BH, int L) {
+    walk_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Walks ws, const Shares sh, const Gate g,
+                   int BH, int L) {
     using K = Cfg<A, B, BWD>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = tc::smem_u32(smem_raw);
@@ -264,19 +267,52 @@ __global__ void __launch_bounds__(THREADS, 1)
     __shared__ volatile int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, gtid = tid & 127;
-    // ---- blockIdx.x = (head, segment in walking order, walk)
-    const int wi = blockIdx.x % ws.n, rest = blockIdx.x / ws.n;
-    const int segs = OUT ? sg.n : (sg.n - 1) * sg.fine, per = OUT ? sg.chunks : sg.chunks / sg.fine;
-    const int seg = rest % segs, bh = rest / segs;
-    const Walk &w = ws.w[wi];
-    const bool rev = w.rev != 0, split = BWD && w.dot != nullptr;
+    // ---- this CTA's chunks, [p0, p1) of the row of all walks' chunks, or a part of such a share's last stretch
     const int NC = (L + C - 1) / C;
-    const int i0 = seg * per, cnt = min(NC, i0 + per) - i0;
-    // Without output the state's weights are taken up to the segment's end, from its last chunk backwards, so
+    const int share = OUT ? blockIdx.x : blockIdx.x / sh.fine;
+    auto bound = [&](int c) { return c * sh.size + min(c, sh.more); };
+    long long p0 = bound(share), p1 = bound(share + 1);
+    // A place in it: the walk and its head, and the chunk's position in walking order.
+    const uint32_t revs = ws.w[0].rev | ws.w[1].rev << 1 | ws.w[2].rev << 2;
+    struct Place {
+        int wi, bh, k;
+        bool rev;
+        __device__ __forceinline__ void walk(int n, uint32_t revs) {  // on to the next walk
+            if (++wi == n) {
+                wi = 0;
+                ++bh;
+            }
+            rev = revs >> wi & 1;
+        }
+        __device__ __forceinline__ int chunk(int NC) const { return rev ? NC - 1 - k : k; }
+    };
+    Place at;
+    {
+        // whole walks: a share is one; shares of cut ones are counted in 32 bits (tc_shares)
+        const uint32_t u = sh.fine == 0 ? share : (uint32_t)(OUT ? p0 : p1 - 1) / (uint32_t)NC;
+        at.k = (int)(p0 - (long long)u * NC);
+        if (!OUT) {
+            const bool ends = p1 == (long long)(u + 1) * NC;  // the share ends with a walk's end: nothing to do
+            if (at.k < 0) at.k = 0;
+            const int len = ends ? 0 : (int)(p1 - (long long)u * NC) - at.k, part = (len + sh.fine - 1) / sh.fine;
+            at.k += part * (blockIdx.x % sh.fine);
+            p0 = (long long)u * NC + at.k;
+            p1 = len > 0 ? min(p1, p0 + part) : p0;
+        }
+        at.bh = u / ws.n;
+        at.wi = u - at.bh * ws.n;
+        at.rev = revs >> at.wi & 1;
+    }
+    const int cnt = p1 > p0 ? (int)(p1 - p0) : 0;
+    // Without output the state's weights are taken up to the stretch's end, from its last chunk backwards, so
     // that every product simply adds to the accumulator.
-    auto chunk = [&](int i) {
-        const int k = OUT ? i0 + i : i0 + cnt - 1 - i;
-        return rev ? NC - 1 - k : k;
+    if (!OUT) at.k += max(cnt - 1, 0);
+    auto next = [&](Place &p) {
+        if (!OUT) --p.k;
+        else if (++p.k == NC) {
+            p.k = 0;
+            p.walk(ws.n, revs);
+        }
     };
 
     if (tid == 0) {
@@ -285,9 +321,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS_FOUR ? 4 : i < BARS_OUT ? (OUT ? 8 : 16) : i < BARS_Y ? (OUT ? 4 : 16) : (OUT ? 2 : 1));
         tc::fence_mbar_init();
         abort_flag = 0;
-        tc::tma_prefetch_desc(&maps.x[wi]);
-        tc::tma_prefetch_desc(&maps.y[wi]);
-        tc::tma_prefetch_desc(&maps.z[wi]);
+        tc::tma_prefetch_desc(&maps.x[at.wi]);
+        tc::tma_prefetch_desc(&maps.y[at.wi]);
+        tc::tma_prefetch_desc(&maps.z[at.wi]);
     }
     if (warp == 0) {
         tc::tmem_alloc(&tmem_base, 512);
@@ -300,11 +336,60 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity & 1, &abort_flag); };
     auto wait_gate = [&](int n) { return n % GB != 0 || wait(&bars.gready[n / GB & 1], n / SLOTS); };
 
+    // The state that enters a walk, or a place in it over the stretches [f0, f1) before it, into tensor memory:
+    // blocks of 16 columns from cb0 on, every `step`.
+    auto load_state = [&](const Place &pl, int f0, int f1, int cb0, int step) {
+        const int j = acc_row<B>(warp & 3, lane);
+        const Walk &w = ws.w[pl.wi];
+        const float *s0 = w.s0 ? w.s0 + (size_t)pl.bh * A * B : nullptr;
+        const int di = w.s0_t ? 1 : B, dj = w.s0_t ? A : 1;
+#pragma unroll 1
+        for (int cb = cb0; cb < A; cb += step) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = s0 && j >= 0 ? s0[(cb + i) * di + j * dj] : 0.f;
+#pragma unroll 1
+            for (int f = f0; f < f1; ++f) {
+                const float e = sh.e[f];
+                const float *u = sh.u + (size_t)f * A * B + (size_t)cb * B + j;
+                if (j >= 0)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = fmaf(e, v[i], u[i * B]);
+            }
+            tc::tmem_st16(tmem + lane_base + K::T_S + cb, v);
+        }
+    };
+    auto store_state = [&](const Place &pl) {
+        const int j = acc_row<B>(warp & 3, lane);
+        float *out = ws.w[pl.wi].s_end ? ws.w[pl.wi].s_end + (size_t)pl.bh * A * B : nullptr;
+        if (!out) return;
+#pragma unroll 1
+        for (int cb = 0; cb < A; cb += 16) {
+            float v[16];
+            tc::tmem_ld16(tmem + lane_base + K::T_S + cb, v);
+            if (j >= 0)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) out[(size_t)(cb + i) * B + j] = v[i];
+        }
+    };
+
+    if (OUT) {
+        cudaGridDependencySynchronize();
+        if (wg >= 2 && wg < 5) {  // the three warpgroups that write and read the state and the outputs
+            int c0 = share;       // the first share whose last stretch is of this walk
+            if (at.k > 0)
+                while (bound(c0) > p0 - at.k) --c0;
+            load_state(at, c0 * sh.fine, share * sh.fine, 16 * (wg - 2), 48);
+            tc::tc_fence_before();
+            tc::named_bar_sync(1, 384);
+            tc::tc_fence_after();
+        }
+    }
     if (warp == W_TMA) {
         const bool leader = elect();
         int n = 0;
         for (; n < cnt; ++n) {
-            const int st = n % NS, c0 = chunk(n) * C;
+            const int st = n % NS, c0 = at.chunk(NC) * C, wi = at.wi, bh = at.bh;
             if (n >= NS && !wait(&bars.free_s[st], n / NS - 1)) break;
             uint8_t *s = base + st * K::STAGE;
             if (leader) {
@@ -314,6 +399,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::tma_load_4d(s + K::OFF_Z, &maps.z[wi], &bars.full[st], 0, c0, 0, bh);
             }
             __syncwarp();
+            next(at);
         }
         if (abort_flag)  // let this CTA's own copies land before it exits (bounded)
             for (int m = n > NS ? n - NS : 0; m < n; ++m) tc::mbar_wait(&bars.full[m % NS], (m / NS) & 1, budget / 8);
@@ -330,12 +416,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tc_fence_after();
             if (leader) {  // S^T += Z^T Yw
                 const uint64_t yw = dw + (uint64_t)((n & 1) * (2 * K::XB >> 4));
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + (h * (K::XB >> 4) + kk * 128), id_s,
-                                     OUT || n > 0 || h > 0 || kk > 0);
+#pragma unroll 1
+                for (int kk = 0; kk < 4; ++kk) {
+                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + kk * 128, id_s, OUT || n > 0 || kk > 0);
+                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + ((K::XB >> 4) + kk * 128), id_s, 1u);
+                }
                 tc::mma_commit(&bars.d2done);
                 tc::mma_commit(&bars.y_free[n & 1]);
             }
@@ -344,17 +429,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int ob = n % K::NO1, m = n - K::NO1;  // read by the output of chunk m
                 if (m >= 0 && !wait(&bars.o_free[m & 1], m >> 1)) break;
                 tc::tc_fence_after();
+                const bool split = BWD && ws.w[at.wi].dot;
                 if (leader) {  // O1^T = S^T X^T
                     const uint32_t o1 = tmem + K::T_O1 + ob * 64;
-#pragma unroll
-                    for (int kk = 0; kk < A / 16; ++kk)
-                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4),
-                                       id_o1, kk > 0);
-                    if (BWD && split) {
-#pragma unroll
-                        for (int kk = 0; kk < A / 16; ++kk)
-                            tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8,
-                                           dx + o + (((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id_o1, 1u);
+#pragma unroll 1
+                    for (int kk = 0; kk < A / 16; ++kk) {
+                        const uint64_t x = dx + o + ((kk >> 2) * 512 + (kk & 3) * 2);
+                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, x, id_o1, kk > 0);
+                        if (split) tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8, x, id_o1, 1u);
                     }
                     tc::mma_commit(&bars.d1done);
                     tc::mma_commit(&bars.o1done[n & 1]);
@@ -362,6 +444,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (leader) tc::mma_commit(&bars.free_s[st]);
             __syncwarp();
+            if (OUT) next(at);
             if (++st == NS) {
                 st = 0;
                 ++ph;
@@ -379,19 +462,18 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto issue_p = [&](int n, int st) {  // P = X Y^T
             if (leader) {
                 const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < A / 16; ++kk) {
-                    const uint32_t off = ((kk >> 2) * 8192 + (kk & 3) * 32) >> 4;
+                    const uint32_t off = (kk >> 2) * 512 + (kk & 3) * 2;
                     tc::mma_bf16(tmem + K::T_P + (n & 1) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
                 }
                 tc::mma_commit(&bars.pdone[n & 1]);
             }
             __syncwarp();
         };
-        if (wait(&bars.full[0], 0)) issue_p(0, 0);
-        int st = 0, ph = 0;
-        for (int n = 0; n < cnt; ++n) {
-            const int cur = st;
+        int st = -1, cur = 0, ph = 0;
+        for (int n = -1; n < cnt; ++n) {
+            cur = st;
             if (++st == NS) {
                 st = 0;
                 ++ph;
@@ -401,11 +483,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::tc_fence_after();
                 issue_p(n + 1, st);
             }
+            if (n < 0) continue;
             if (!wait(&bars.p_ready, n) || (n > 0 && !wait(&bars.o_free[(n - 1) & 1], (n - 1) >> 1))) break;
             tc::tc_fence_after();
             if (leader) {  // O2^T = Z^T (D o P)^T
                 const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));
-#pragma unroll
+#pragma unroll 1
                 for (int kk = 0; kk < 4; ++kk)
                     tc::mma_bf16(tmem + K::T_O2, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
                 tc::mma_commit(&bars.o2done);
@@ -418,69 +501,100 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         tc::mbar_wait(&bars.drain[1], 0, budget / 4);
     } else if (warp == W_GATE) {
-        // Four chunks at once: eight lanes a chunk, eight tokens a lane (one chunk at a time, in pairs of tokens,
-        // took 3000 cycles a chunk: a long dependent stretch of code that runs once).
-        Fixed sum = 0;
-        bool good = true;
-        float l[8];
+        // Four chunks at once: eight lanes a chunk, eight tokens a lane.  A weight is 2 to the sum of the log-decays
+        // between its token and the chunk's start or end, and each is summed from that side: fp32 rounds a sum
+        // by 2^-24 of itself, and where that is much the weight is nothing.
+        float sum = 0.f;
+        float x[8];
         const int gk = lane >> 3, tk = 8 * (lane & 7);  // this lane's chunk of the four, and its first token in it
-        auto load = [&](int n) {
-            const int t = n + gk < cnt ? chunk(n + gk) * C + tk : L;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) l[i] = gate_or_zero(g, bh, L, t + i);
-        };
-        load(0);
-        for (int n = 0; n < cnt; n += GB) {
-            Fixed c[8];
-            int bad = C;  // the first token of the chunk whose log-decay is not a number: later sums are not either
-#pragma unroll
-            for (int i = 7; i >= 0; --i) {
-                c[i] = to_fixed(l[i]);
-                if (l[i] != l[i]) bad = tk + i;
+        const __nv_bfloat16 *tokens = static_cast<const __nv_bfloat16 *>(g.p);
+        const float *heads = static_cast<const float *>(g.p);
+        Place pl = at;  // of the lane's chunk in the batch that is loaded
+        bool rev;       // of its chunk in the batch that is worked on
+        auto load = [&](int n, int skip) {
+            if (!OUT) pl.k -= skip;
+            else {
+#pragma unroll 1
+                for (pl.k += skip; pl.k >= NC; pl.k -= NC) pl.walk(ws.n, revs);
             }
-            if (n + GB < cnt) load(n + GB);
+            const int t = n + gk < cnt ? pl.chunk(NC) * C + tk : L;
+            const float lh = g.per_head && t < L ? heads[pl.bh % g.H] : 0.f;
+            const __nv_bfloat16 *row = tokens + (size_t)pl.bh * L;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = lh;
+                if (!g.per_head && t + i < L) x[i] = __bfloat162float(row[t + i]);
+                if (t + i >= L) x[i] = 0.f;
+            }
+        };
+        load(0, gk);
+        for (int n = 0; n < cnt; n += GB) {
+            float c[8], d[8];  // sums up to and with the token, and behind it, in units of log 2, of this lane's eight
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float l = x[i] < L_MIN ? L_MIN : x[i] > -L_MIN ? -L_MIN : x[i];  // NaN stays NaN
+                c[i] = l * 1.44269504f;
+            }
+            rev = pl.rev;
+            if (n + GB < cnt) load(n + GB, GB);
+            d[7] = 0.f;
+#pragma unroll
+            for (int i = 6; i >= 0; --i) d[i] = d[i + 1] + c[i + 1];
+            const float own = d[0] + c[0], first = c[0];
 #pragma unroll
             for (int i = 1; i < 8; ++i) c[i] += c[i - 1];
-            Fixed s = c[7];
+            float before = own, behind = own;  // inclusive, over the chunk's eight lanes from either side
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1) {
-                const Fixed y = __shfl_up_sync(0xffffffffu, s, o, 8);
-                if ((lane & 7) >= o) s += y;
-                bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, o));
+                const float u = __shfl_up_sync(0xffffffffu, before, o, 8), v = __shfl_down_sync(0xffffffffu, behind, o, 8);
+                if ((lane & 7) >= o) before += u;
+                if ((lane & 7) < 8 - o) behind += v;
             }
-            const Fixed before = s - c[7], cC = __shfl_sync(0xffffffffu, s, 7, 8);
+            const float cC = __shfl_sync(0xffffffffu, before, 7, 8);
+            before = __shfl_up_sync(0xffffffffu, before, 1, 8);
+            behind = __shfl_down_sync(0xffffffffu, behind, 1, 8);
+            if ((lane & 7) == 0) before = 0.f;
+            if ((lane & 7) == 7) behind = 0.f;
             float after = 1.f;
             if (!OUT) {  // the decay of the chunks already walked, the batch's earlier ones among them
 #pragma unroll
                 for (int k = 0; k < GB; ++k) {
-                    if (k == gk) after = if_good(exp2_fixed(sum), good);
-                    sum = max(sum + __shfl_sync(0xffffffffu, cC, 8 * k), FIXED_MIN);
-                    good = good && __shfl_sync(0xffffffffu, bad, 8 * k) == C;
+                    if (k == gk) after = ex2(sum);
+                    sum += __shfl_sync(0xffffffffu, cC, 8 * k);
                 }
             }
             const int bi = n / GB & 1;
             if (n >= SLOTS && !wait(&bars.gfree[bi], n / SLOTS - 1)) break;
             Slot &sl = slots[bi * GB + gk];
-            const Fixed ce = before + (rev ? c[0] : c[7]);
+            float *up = (rev ? sl.kw : sl.qw) + tk, *down = (rev ? sl.qw : sl.kw) + tk;
+            if (OUT || rev) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const Fixed x = before + c[i];
-                const float up = if_good(ex2_fixed(x), tk + i < bad), down = if_good(ex2_fixed(cC - x), bad == C || tk + i >= bad);
-                sl.kw[tk + i] = (rev ? up : down) * after;
-                if (OUT) {
-                    sl.qw[tk + i] = rev ? down : up;
-                    sl.gw[tk + i] = ex2_fixed(rev ? x - ce : ce - x);
-                    const float h = __ll2float_rn(x) * (1.f / FIXED_ONE);
-                    sl.c2[tk + i] = if_good(rev ? -h : h, tk + i < bad);
-                }
+                for (int i = 0; i < 8; i += 4)
+                    *reinterpret_cast<float4 *>(up + i) = make_float4(after * ex2(before + c[i]), after * ex2(before + c[i + 1]),
+                                                                     after * ex2(before + c[i + 2]), after * ex2(before + c[i + 3]));
             }
-            if (OUT && (lane & 7) == 0) sl.tot = if_good(ex2_fixed(cC), bad == C);
+            if (OUT || !rev) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 4)
+                    *reinterpret_cast<float4 *>(down + i) = make_float4(after * ex2(behind + d[i]), after * ex2(behind + d[i + 1]),
+                                                                       after * ex2(behind + d[i + 2]), after * ex2(behind + d[i + 3]));
+            }
+            if (OUT) {
+                const float sg = rev ? -1.f : 1.f;
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    *reinterpret_cast<float4 *>(sl.c2 + tk + i) = make_float4(sg * (before + c[i]), sg * (before + c[i + 1]),
+                                                                              sg * (before + c[i + 2]), sg * (before + c[i + 3]));
+                    // within the lane's eight: behind a token, or between the first and it
+                    *reinterpret_cast<float4 *>(sl.gw + tk + i) = make_float4(ex2(rev ? c[i] - first : d[i]), ex2(rev ? c[i + 1] - first : d[i + 1]),
+                                                                              ex2(rev ? c[i + 2] - first : d[i + 2]), ex2(rev ? c[i + 3] - first : d[i + 3]));
+                }
+                if ((lane & 7) == 0) sl.tot = ex2(cC);
+            }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars.gready[bi]);
         }
-        // every walk in the same direction finds the same decay of a segment: its first one writes it
-        if (!OUT && lane == 0 && (wi == 0 || ws.w[wi - 1].rev != w.rev))
-            sg.e[((size_t)(rev ? 1 : 0) * BH + bh) * segs + seg] = if_good(exp2_fixed(sum), good);
+        if (!OUT && lane == 0) sh.e[blockIdx.x] = ex2(sum);  // 1 for an empty stretch
     } else if (OUT ? wg == 0 : wg < 4) {
         // ---------------------------------------------------------- Yw
         for (int n = 0; n < cnt; ++n) {
@@ -508,7 +622,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!OUT && wg == 0 && wait(&bars.drain[0], 0)) {  // the segment's contribution
             const int j = acc_row<B>(warp, lane);
-            float *sout = w.u + ((size_t)bh * segs + seg) * A * B;
+            float *sout = sh.u + (size_t)blockIdx.x * A * B;
             tc::tc_fence_after();
 #pragma unroll 1
             for (int cb = 0; cb < A; cb += 16) {
@@ -516,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::tmem_ld16(tmem + lane_base + K::T_S + cb, v);
                 if (j >= 0)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sout[(size_t)(cb + i) * B + j] = v[i];
+                    for (int i = 0; i < 16; ++i) sout[(size_t)(cb + i) * B + j] = cnt > 0 ? v[i] : 0.f;
             }
         }
     } else if (OUT && wg == 1) {
@@ -527,13 +641,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         // eight: neither factor grows, and the second is made once a chunk.  The off side stays zero.
         const int r0 = 16 * (warp & 3), r = r0 + (lane >> 2), cq = 2 * (lane & 3);
         uint8_t *pt = base + K::OFF_P;
-        {
+        bool rev = false;
+        int on0 = 0, on1 = 0;  // columns of the on side's blocks
+        for (int n = 0; n < cnt; ++n, next(at)) {
+            if (n == 0 || at.rev != rev) {  // the other direction: the off side anew
+                if (n > 0 && !wait(&bars.o2done, n - 1)) break;
+                rev = at.rev;
 #pragma unroll 1
-            for (int c = rev ? 0 : 2 * (warp & 3) + 2; c < (rev ? 2 * (warp & 3) : 8); ++c)
-                *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r0 + (lane & 15), c)) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        const int on0 = rev ? r0 + 16 : 0, on1 = rev ? 64 : r0;  // columns of the on side's blocks
-        for (int n = 0; n < cnt; ++n) {
+                for (int c = rev ? 0 : 2 * (warp & 3) + 2; c < (rev ? 2 * (warp & 3) : 8); ++c)
+                    *reinterpret_cast<uint4 *>(pt + tc::sw128_off(r0 + (lane & 15), c)) = make_uint4(0u, 0u, 0u, 0u);
+                on0 = rev ? r0 + 16 : 0;
+                on1 = rev ? 64 : r0;
+                __syncwarp();
+            }
             if (!wait_gate(n) || !wait(&bars.pdone[n & 1], n >> 1)) break;
             tc::tc_fence_after();
             const Slot &sl = slots[n % SLOTS];
@@ -591,30 +711,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else if (OUT && wg == 2) {
         // ---------------------------------------------------------- S^T
-        const int j = acc_row<B>(warp & 3, lane);
-        const size_t ab = (size_t)A * B;
-        cudaGridDependencySynchronize();
-        const float *sin = sg.n > 1 ? w.in + ((size_t)bh * sg.n + seg) * ab : (w.s0 ? w.s0 + bh * ab : nullptr);
-        const bool st = sg.n == 1 && w.s0_t;
-        bool ok = true;
-        {  // the state that enters, as if a chunk had left it
-#pragma unroll 1
-            for (int cb = 0; cb < A; cb += 16) {
-                float v[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    v[i] = sin && j >= 0 ? (st ? sin[(size_t)j * A + cb + i] : sin[(size_t)(cb + i) * B + j]) : 0.f;
-                tc::tmem_st16(tmem + lane_base + K::T_S + cb, v);
+        for (int n = 0;; ++n, next(at)) {
+            if (n > 0) {
+                if (!wait(&bars.d2done, n - 1)) break;
+                tc::tc_fence_after();
+                if (at.k == 0) {  // the end of a walk: its state leaves
+                    Place last = at;
+                    last.bh = at.wi > 0 ? at.bh : at.bh - 1;
+                    last.wi = at.wi > 0 ? at.wi - 1 : ws.n - 1;
+                    store_state(last);
+                    if (n < cnt) load_state(at, 0, 0, 0, 16);
+                }
             }
-        }
-        for (int n = 0; ok && n < cnt; ++n) {
-            ok = wait_gate(n) && (n == 0 || wait(&bars.d2done, n - 1));
-            if (!ok) break;
-            tc::tc_fence_after();
+            if (n == cnt || !wait_gate(n)) break;
             const F2 tot2 = f2(slots[n % SLOTS].tot, slots[n % SLOTS].tot);
             if (n > 0) {  // the copy's last reader
-                ok = wait(&bars.d1done, n - 1);
-                if (!ok) break;
+                if (!wait(&bars.d1done, n - 1)) break;
                 tc::tc_fence_after();
             }
 #pragma unroll 1
@@ -625,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) split2(f2(v[2 * i], v[2 * i + 1]), h[i], l[i]);
                 tmem_st16(tmem + lane_base + K::T_H + cb / 2, h);
-                if (BWD && split) tmem_st16(tmem + lane_base + K::T_L + cb / 2, l);
+                if (BWD && ws.w[at.wi].dot) tmem_st16(tmem + lane_base + K::T_L + cb / 2, l);
 #pragma unroll
                 for (int e = 0; e < 32; e += 16) {
                     uint32_t u[16];
@@ -641,32 +753,30 @@ __global__ void __launch_bounds__(THREADS, 1)
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             warp_arrive(&bars.s_ready, lane);
         }
-        float *sout = seg == sg.n - 1 && w.s_end ? w.s_end + bh * ab : nullptr;
-        if (ok && sout && wait(&bars.d2done, cnt - 1)) {
-            tc::tc_fence_after();
-#pragma unroll 1
-            for (int cb = 0; cb < A; cb += 16) {
-                float v[16];
-                tc::tmem_ld16(tmem + lane_base + K::T_S + cb, v);
-                if (j >= 0)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) sout[(size_t)(cb + i) * B + j] = v[i];
-            }
-        }
     } else if (OUT && (wg == 3 || wg == 4)) {
         // ---------------------------------------------------------- out
         const int j = acc_row<B>(warp & 3, lane), h0 = wg == 3 ? 0 : 32;  // tokens h0 .. h0 + 31 of a chunk
         for (int n = 0; n < cnt; ++n) {
-            const int t0 = chunk(n) * C + h0, cl = min(32, L - t0);
+            const int t0 = at.chunk(NC) * C + h0, cl = min(32, L - t0), bh = at.bh;
+            const Walk &w = ws.w[at.wi];
+            const bool split = BWD && w.dot != nullptr;
             const size_t row0 = (size_t)bh * L + t0;
+            next(at);
             uint32_t xr[16];  // this lane's elements of the dots' other factor, two tokens a word
-            if (BWD && split) {
+            if (split) {
                 const unsigned short *dx = static_cast<const unsigned short *>(w.dotx) + row0 * B + j;
+                const int xl = j >= 0 ? cl : 0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const uint32_t a = j >= 0 && 2 * i < cl ? dx[2 * i * B] : 0, b = j >= 0 && 2 * i + 1 < cl ? dx[(2 * i + 1) * B] : 0;
-                    xr[i] = a | (b << 16);
+                    const uint32_t a = 2 * i < xl ? dx[2 * i * B] : 0, b = 2 * i + 1 < xl ? dx[(2 * i + 1) * B] : 0;
+                    xr[i] = a | b << 16;
                 }
+                // the next chunk's on their way to L2: a row of this warp's columns a lane
+                const Walk &nw = ws.w[at.wi];
+                const int t = at.chunk(NC) * C + h0 + lane;
+                if (n + 1 < cnt && nw.dot && t < L)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const unsigned short *>(nw.dotx) +
+                                                                  ((size_t)at.bh * L + t) * B + (B / 4) * (warp & 3)));
             }
             if (!wait_gate(n) || !wait(&bars.o1done[n & 1], n >> 1) || !wait(&bars.o2read, n)) break;
             tc::tc_fence_after();
@@ -690,16 +800,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
             if (j >= 0) {
                 TO *out = static_cast<TO *>(w.out) + row0 * B + j;
-                if (cl == 32) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < cl) put(out + i * B, v[i]);
-                }
+                for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], i < cl, i + 1 < cl);
             }
-            if (BWD && split) {
+            if (split) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     v[2 * i] = j >= 0 ? v[2 * i] * bf_lo(xr[i]) : 0.f;
@@ -717,20 +821,19 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 template <int A, int B, typename TO, bool BWD>
-cudaError_t launch_t(const Maps &maps, const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out, cudaStream_t s) {
+cudaError_t launch_t(const Maps &maps, const Walks &ws, Gate g, int BH, int L, const Shares &sh, bool out, cudaStream_t s) {
     constexpr int smem = Cfg<A, B, BWD>::SMEM;
     auto *kernel = out ? walk_tc_kernel<A, B, TO, true, BWD> : walk_tc_kernel<A, B, TO, false, BWD>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     count_launches(1);
-    const dim3 grid((unsigned)BH * (out ? sg.n : sg.stretches()) * ws.n);
-    if (out && sg.n > 1) return launch_after(kernel, grid, THREADS, smem, s, maps, ws, sg, g, BH, L);
-    kernel<<<grid, THREADS, smem, s>>>(maps, ws, sg, g, BH, L);
+    if (out && sh.stretches() > 0) return launch_after(kernel, dim3(sh.g), THREADS, smem, s, maps, ws, sh, g, BH, L);
+    kernel<<<out ? sh.g : sh.stretches(), THREADS, smem, s>>>(maps, ws, sh, g, BH, L);
     return cudaGetLastError();
 }
 
 template <typename TO, bool BWD>
-cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out, cudaStream_t s) {
+cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, const Shares &sh, bool out, cudaStream_t s) {
     Maps maps;
     for (int i = 0; i < ws.n; ++i) {
         const Walk &w = ws.w[i];
@@ -739,62 +842,50 @@ cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, const Segments &sg
             return cudaErrorInvalidValue;
     }
     const int a = ws.w[0].a, b = ws.w[0].b;
-    if (a == 128 && b == 128) return launch_t<128, 128, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
-    if (a == 128) return launch_t<128, 64, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
-    if (b == 128) return launch_t<64, 128, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
-    return launch_t<64, 64, TO, BWD>(maps, ws, g, BH, L, sg, out, s);
+    if (a == 128 && b == 128) return launch_t<128, 128, TO, BWD>(maps, ws, g, BH, L, sh, out, s);
+    if (a == 128) return launch_t<128, 64, TO, BWD>(maps, ws, g, BH, L, sh, out, s);
+    if (b == 128) return launch_t<64, 128, TO, BWD>(maps, ws, g, BH, L, sh, out, s);
+    return launch_t<64, 64, TO, BWD>(maps, ws, g, BH, L, sh, out, s);
 }
 
-cudaError_t launch_pass(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out_bf16, bool bwd, bool out,
+cudaError_t launch_pass(const Walks &ws, Gate g, int BH, int L, const Shares &sh, bool out_bf16, bool bwd, bool out,
                         cudaStream_t s) {
-    // walks of the same head sizes share a launch
-    Walks part{};
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < ws.n && e == cudaSuccess; ++i) {
-        part.w[part.n++] = ws.w[i];
-        if (i + 1 < ws.n && ws.w[i + 1].a == ws.w[i].a && ws.w[i + 1].b == ws.w[i].b) continue;
-        if (bwd) e = launch_ab<__nv_bfloat16, true>(part, g, BH, L, sg, out, s);
-        else if (out_bf16) e = launch_ab<__nv_bfloat16, false>(part, g, BH, L, sg, out, s);
-        else e = launch_ab<float, false>(part, g, BH, L, sg, out, s);
-        part.n = 0;
-    }
-    return e;
+    if (bwd) return launch_ab<__nv_bfloat16, true>(ws, g, BH, L, sh, out, s);
+    if (out_bf16) return launch_ab<__nv_bfloat16, false>(ws, g, BH, L, sh, out, s);
+    return launch_ab<float, false>(ws, g, BH, L, sh, out, s);
 }
 
 }  // namespace
 
 bool tc_sizes(int dk, int dv, bool bf16) { return bf16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128); }
 
-Segments tc_segments(int BH, int L, int n) {
-    // One CTA an SM.  Cutting a sequence costs a first pass (the state's contributions alone), so it is cut
-    // only as far as its CTAs still fit the device at once, at four chunks a segment or more; the first
-    // pass's stretches then fill the device too, at two chunks each or more.
-    const long long units = (long long)BH * n;
-    const int NC = (L + C - 1) / C;
-    Segments sg{};
-    sg.chunks = NC;
-    long long want = 148 / units;
-    if (want > NC / 4) want = NC / 4;
-    if (want < 2) return sg;
-    int per = (int)((NC + want - 1) / want), m = (NC + per - 1) / per;
-    long long fine = 148 / (units * (m - 1));
-    if (fine > per / 2) fine = per / 2;
-    if (fine < 1) fine = 1;
-    sg.fine = (int)fine;
-    sg.chunks = (per + sg.fine - 1) / sg.fine * sg.fine;
-    sg.n = (NC + sg.chunks - 1) / sg.chunks;
-    return sg;
+Shares tc_shares(int BH, int L, int n) {
+    // In chunks of a walk: whole walks take as many rounds as the device needs for them; even shares take their
+    // length and the first pass, whose chunks cost 0.4 of a walk's and whose stretches are at most a share or a
+    // walk, in halves (two CTAs an SM follow one another), and some 6 for its launch and the states between.
+    constexpr int SMS = 148;
+    const long long units = (long long)BH * n, NC = (L + C - 1) / C, total = units * NC;
+    Shares sh{};
+    sh.g = (int)units;
+    sh.size = NC;
+    const long long g = total / 4 < SMS ? total / 4 : SMS;  // four chunks a share or more
+    if (g < 2 || total >= 1LL << 31) return sh;
+    const double whole = (double)((units + SMS - 1) / SMS * NC), even = (double)total / g;
+    if (even + 0.4 * (even < NC ? even : 0.7 * NC) + 6. >= whole) return sh;
+    sh.g = (int)g;
+    sh.size = total / g;
+    sh.more = (int)(total % g);
+    sh.fine = even < NC ? 1 : 2;
+    return sh;
 }
 
-cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, const Segments &sg, bool out_bf16, bool bwd,
+cudaError_t launch_walks_tc(const Walks &ws, Gate g, int BH, int L, const Shares &sh, bool out_bf16, bool bwd,
                             cudaStream_t s) {
-    cudaError_t e = cudaSuccess;
-    if (sg.n > 1) {
-        e = launch_pass(ws, g, BH, L, sg, out_bf16, bwd, false, s);
-        if (e == cudaSuccess) e = launch_seg_chain(ws, sg, BH, s);
+    if (sh.stretches() > 0) {
+        const cudaError_t e = launch_pass(ws, g, BH, L, sh, out_bf16, bwd, false, s);
         if (e != cudaSuccess) return e;
     }
-    return launch_pass(ws, g, BH, L, sg, out_bf16, bwd, true, s);
+    return launch_pass(ws, g, BH, L, sh, out_bf16, bwd, true, s);
 }
 
 cudaError_t read_and_clear_error(unsigned int *out) {

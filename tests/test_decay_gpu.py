@@ -45,7 +45,7 @@ def make(B, H, L, dk, dv, dtype, form="token", s0=False, seed=0, level=3.0):
 
 SIZES = [(1, 1, 1, 64, 64), (2, 3, 63, 64, 64), (1, 2, 64, 128, 128), (1, 2, 65, 128, 64), (2, 1, 200, 64, 128),
          (1, 3, 130, 40, 24), (1, 2, 333, 17, 33), (1, 1, 70, 1, 1), (1, 1, 1000, 128, 128), (1, 2, 2100, 64, 64),
-         (40, 4, 130, 128, 128)]
+         (40, 4, 130, 128, 128), (5, 13, 1500, 64, 64), (1, 149, 700, 64, 128)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -158,7 +158,8 @@ def test_step(size, form, dtype):
 
 
 GRAD_SIZES = [(1, 1, 1, 64, 64), (1, 2, 65, 64, 64), (1, 2, 200, 128, 128), (1, 1, 130, 128, 64), (2, 1, 100, 64, 128),
-              (1, 2, 90, 20, 12), (1, 1, 333, 33, 17), (1, 1, 1100, 64, 64), (24, 8, 70, 128, 128)]
+              (1, 2, 90, 20, 12), (1, 1, 333, 33, 17), (1, 1, 1100, 64, 64), (24, 8, 70, 128, 128), (5, 13, 1500, 64, 64),
+              (3, 25, 900, 64, 128)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
