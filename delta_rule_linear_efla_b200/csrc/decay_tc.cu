@@ -75,18 +75,19 @@ struct Cfg {
 
 struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
-    uint64_t full[NS], gready[2], y_free[2], pdone[2], d1done, d2done, o1done[2], o2done, o2read, drain[2];
+    uint64_t full[NS], gready[2], y_free[2], pdone[2], d2done, o1done[2], o2done, o2read, drain[2];
     // one arrival from each of four warps
     uint64_t p_ready, s_ready;
     uint64_t gfree[2], o_free[2];  // the eight output warps (without output, gfree: the weights' sixteen)
     uint64_t y_ready[2];               // the weights' four warps, sixteen without output
     uint64_t free_s[NS];               // one from each issuer
 };
-constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 2 + 2 + 2 + 2, BARS_FOUR = BARS_ONE + 2,
+constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 1 + 2 + 2 + 2, BARS_FOUR = BARS_ONE + 2,
               BARS_OUT = BARS_FOUR + 2 + 2, BARS_Y = BARS_OUT + 2;
 
 struct Slot {
-    float qw[C], kw[C];
+    float qw[C];
+    uint32_t kw[C];  // a key's weight as two bf16: hi (low half) + lo
     float gw[C];  // 2^(c_end - c) within a token's group of eight (end: its last token in walking order)
     float c2[C];  // running sum in units of log 2 (its negative backwards)
     float tot, pad[3];
@@ -225,6 +226,15 @@ __device__ __forceinline__ uint32_t pack(F2 a) {
 __device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
     hi = pack(x);
     lo = pack(fma2(f2(bf_lo(hi), bf_hi(hi)), f2(-1.f, -1.f), x));
+}
+
+// Two bf16 times a weight given as two bf16, fh + fl: hi + lo to 2^-17.  hi rounds y fh; what that leaves of the
+// 16-bit product is exact in bf16, and lo adds y fl to it.
+__device__ __forceinline__ void weigh(uint32_t y, uint32_t fh, uint32_t fl, uint32_t &hi, uint32_t &lo) {
+    uint32_t rest;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(fh));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(rest) : "r"(y), "r"(fh), "r"(hi ^ 0x80008000u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(y), "r"(fl), "r"(rest));
 }
 
 // The sums over a warp's lanes of 32 columns: lane l ends with column l's.
@@ -412,7 +422,27 @@ __global__ void __launch_bounds__(THREADS, 1)
         int st = 0, ph = 0;  // stage and its pass
         for (int n = 0; n < cnt; ++n) {
             const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-            if (!wait(&bars.full[st], ph) || !wait(&bars.y_ready[n & 1], n >> 1) || (OUT && !wait(&bars.s_ready, n))) break;
+            if (!wait(&bars.full[st], ph) || (OUT && !wait(&bars.s_ready, n))) break;
+            tc::tc_fence_after();
+            if (OUT) {
+                // O1^T = S^T X^T, before the state changes: its copy is then free when the new state is there
+                const int ob = n % K::NO1, m = n - K::NO1;  // read by the output of chunk m
+                if (m >= 0 && !wait(&bars.o_free[m & 1], m >> 1)) break;
+                tc::tc_fence_after();
+                const bool split = BWD && ws.w[at.wi].dot;
+                if (leader) {
+                    const uint32_t o1 = tmem + K::T_O1 + ob * 64;
+#pragma unroll 1
+                    for (int kk = 0; kk < A / 16; ++kk) {
+                        const uint64_t x = dx + o + ((kk >> 2) * 512 + (kk & 3) * 2);
+                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, x, id_o1, kk > 0);
+                        if (split) tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8, x, id_o1, 1u);
+                    }
+                    tc::mma_commit(&bars.o1done[n & 1]);
+                }
+                __syncwarp();
+            }
+            if (!wait(&bars.y_ready[n & 1], n >> 1)) break;
             tc::tc_fence_after();
             if (leader) {  // S^T += Z^T Yw
                 const uint64_t yw = dw + (uint64_t)((n & 1) * (2 * K::XB >> 4));
@@ -423,24 +453,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 tc::mma_commit(&bars.d2done);
                 tc::mma_commit(&bars.y_free[n & 1]);
-            }
-            __syncwarp();
-            if (OUT) {
-                const int ob = n % K::NO1, m = n - K::NO1;  // read by the output of chunk m
-                if (m >= 0 && !wait(&bars.o_free[m & 1], m >> 1)) break;
-                tc::tc_fence_after();
-                const bool split = BWD && ws.w[at.wi].dot;
-                if (leader) {  // O1^T = S^T X^T
-                    const uint32_t o1 = tmem + K::T_O1 + ob * 64;
-#pragma unroll 1
-                    for (int kk = 0; kk < A / 16; ++kk) {
-                        const uint64_t x = dx + o + ((kk >> 2) * 512 + (kk & 3) * 2);
-                        tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, x, id_o1, kk > 0);
-                        if (split) tc::mma_tmem_a(o1, tmem + K::T_L + kk * 8, x, id_o1, 1u);
-                    }
-                    tc::mma_commit(&bars.d1done);
-                    tc::mma_commit(&bars.o1done[n & 1]);
-                }
             }
             if (leader) tc::mma_commit(&bars.free_s[st]);
             __syncwarp();
@@ -566,18 +578,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int bi = n / GB & 1;
             if (n >= SLOTS && !wait(&bars.gfree[bi], n / SLOTS - 1)) break;
             Slot &sl = slots[bi * GB + gk];
-            float *up = (rev ? sl.kw : sl.qw) + tk, *down = (rev ? sl.qw : sl.kw) + tk;
-            if (OUT || rev) {
 #pragma unroll
-                for (int i = 0; i < 8; i += 4)
-                    *reinterpret_cast<float4 *>(up + i) = make_float4(after * ex2(before + c[i]), after * ex2(before + c[i + 1]),
-                                                                     after * ex2(before + c[i + 2]), after * ex2(before + c[i + 3]));
-            }
-            if (OUT || !rev) {
+            for (int i = 0; i < 8; i += 4) {
+                float q[4];
+                uint32_t k[4];
 #pragma unroll
-                for (int i = 0; i < 8; i += 4)
-                    *reinterpret_cast<float4 *>(down + i) = make_float4(after * ex2(behind + d[i]), after * ex2(behind + d[i + 1]),
-                                                                       after * ex2(behind + d[i + 2]), after * ex2(behind + d[i + 3]));
+                for (int e = 0; e < 4; ++e) {
+                    const float up = ex2(before + c[i + e]), down = ex2(behind + d[i + e]);
+                    const float w = after * (rev ? up : down);
+                    q[e] = rev ? down : up;
+                    const float hi = __bfloat162float(__float2bfloat16_rn(w));
+                    k[e] = tc::pack_bf16(hi, w - hi);
+                }
+                *reinterpret_cast<uint4 *>(sl.kw + tk + i) = make_uint4(k[0], k[1], k[2], k[3]);
+                if (OUT) *reinterpret_cast<float4 *>(sl.qw + tk + i) = make_float4(q[0], q[1], q[2], q[3]);
             }
             if (OUT) {
                 const float sg = rev ? -1.f : 1.f;
@@ -603,16 +617,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint4 *y = reinterpret_cast<const uint4 *>(base + (n % NS) * K::STAGE + K::OFF_Y);
             uint4 *hi = reinterpret_cast<uint4 *>(base + K::OFF_W + (n & 1) * 2 * K::XB);
             uint4 *lo = hi + K::XB / 16;
-            const float *kw = slots[n % SLOTS].kw;
+            const uint32_t *kw = slots[n % SLOTS].kw;
 #pragma unroll 2
             for (int i = OUT ? gtid : tid; i < K::XB / 16; i += OUT ? 128 : 512) {  // 8 pieces of 16 bytes a row of a 64-column slab
-                const F2 f = f2(kw[(i >> 3) & 63], kw[(i >> 3) & 63]);
+                const uint32_t f = kw[(i >> 3) & 63];
+                const uint32_t fh = __byte_perm(f, f, 0x1010), fl = __byte_perm(f, f, 0x3232);
                 const uint4 u = y[i];
                 uint4 h, l;
-                split2(f * f2(bf_lo(u.x), bf_hi(u.x)), h.x, l.x);
-                split2(f * f2(bf_lo(u.y), bf_hi(u.y)), h.y, l.y);
-                split2(f * f2(bf_lo(u.z), bf_hi(u.z)), h.z, l.z);
-                split2(f * f2(bf_lo(u.w), bf_hi(u.w)), h.w, l.w);
+                weigh(u.x, fh, fl, h.x, l.x);
+                weigh(u.y, fh, fl, h.y, l.y);
+                weigh(u.z, fh, fl, h.z, l.z);
+                weigh(u.w, fh, fl, h.w, l.w);
                 hi[i] = h;
                 lo[i] = l;
             }
@@ -725,10 +740,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (n == cnt || !wait_gate(n)) break;
             const F2 tot2 = f2(slots[n % SLOTS].tot, slots[n % SLOTS].tot);
-            if (n > 0) {  // the copy's last reader
-                if (!wait(&bars.d1done, n - 1)) break;
-                tc::tc_fence_after();
-            }
 #pragma unroll 1
             for (int cb = 0; cb < A; cb += 32) {
                 float v[32];
@@ -800,8 +811,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
             if (j >= 0) {
                 TO *out = static_cast<TO *>(w.out) + row0 * B + j;
+                if (cl == 32) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], i < cl, i + 1 < cl);
+                    for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], true, true);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], i < cl, i + 1 < cl);
+                }
             }
             if (split) {
 #pragma unroll
