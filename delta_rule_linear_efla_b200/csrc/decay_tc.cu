@@ -51,6 +51,7 @@ namespace {
 constexpr int WARPS = 24, THREADS = WARPS * 32;
 constexpr int W_STATE = 20, W_INTRA = 21, W_TMA = 22, W_GATE = 23;
 constexpr int NS = 3;     // stages of X, Y, Z
+constexpr int AHEAD = 4;  // chunks that are brought to L2 ahead of their load
 constexpr int GB = 4, SLOTS = 2 * GB;  // chunks whose decay weights are made at once, and kept
 constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
 
@@ -112,10 +113,10 @@ __device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(addr), "r"(parity), "r"(1000000u)
+        : "r"(addr), "r"(parity)
         : "memory");
     return ok != 0;
 }
@@ -341,9 +342,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = tmem_base, lane_base = (uint32_t)(32 * (warp & 3)) << 16, sb = tc::smem_u32(base);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0), lane_base = (uint32_t)(32 * (warp & 3)) << 16, sb = tc::smem_u32(base);
     const long long budget = WAIT_BUDGET;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity & 1, &abort_flag); };
+    // for the issuing warps: the same answer in every lane, so that descriptors stay in uniform registers
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     auto wait_gate = [&](int n) { return n % GB != 0 || wait(&bars.gready[n / GB & 1], n / SLOTS); };
 
     // The state that enters a walk, or a place in it over the stretches [f0, f1) before it, into tensor memory:
@@ -397,8 +400,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (warp == W_TMA) {
         const bool leader = elect();
-        int n = 0;
+        // Tiles come to L2 AHEAD chunks before they are loaded: shared memory holds three chunks, which covers an
+        // L2 read but not one from HBM.
+        Place far = at;
+        int n = 0, m = 0;
         for (; n < cnt; ++n) {
+#pragma unroll 1
+            for (; m < cnt && m < n + AHEAD; ++m) {
+                const int c0 = far.chunk(NC) * C;
+                if (leader && m >= NS) {
+                    tc::tma_prefetch_4d(&maps.y[far.wi], 0, c0, 0, far.bh);
+                    if (OUT) tc::tma_prefetch_4d(&maps.x[far.wi], 0, c0, 0, far.bh);
+                    tc::tma_prefetch_4d(&maps.z[far.wi], 0, c0, 0, far.bh);
+                }
+                next(far);
+            }
             const int st = n % NS, c0 = at.chunk(NC) * C, wi = at.wi, bh = at.bh;
             if (n >= NS && !wait(&bars.free_s[st], n / NS - 1)) break;
             uint8_t *s = base + st * K::STAGE;
@@ -418,21 +434,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true), id_o1 = tc::idesc_bf16(B, 64, false, false);
         const uint64_t dx = tc::sdesc(sb + K::OFF_X, 16, 1024), dz = tc::sdesc(sb + K::OFF_Z, 8192, 1024);
         const uint64_t dw = tc::sdesc(sb + K::OFF_W, 8192, 1024);
-        const bool leader = elect();
         int st = 0, ph = 0;  // stage and its pass
         for (int n = 0; n < cnt; ++n) {
             const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-            if (!wait(&bars.full[st], ph) || (OUT && !wait(&bars.s_ready, n))) break;
+            if (!wait_all(&bars.full[st], ph) || (OUT && !wait_all(&bars.s_ready, n))) break;
             tc::tc_fence_after();
             if (OUT) {
                 // O1^T = S^T X^T, before the state changes: its copy is then free when the new state is there
                 const int ob = n % K::NO1, m = n - K::NO1;  // read by the output of chunk m
-                if (m >= 0 && !wait(&bars.o_free[m & 1], m >> 1)) break;
+                if (m >= 0 && !wait_all(&bars.o_free[m & 1], m >> 1)) break;
                 tc::tc_fence_after();
                 const bool split = BWD && ws.w[at.wi].dot;
-                if (leader) {
+                if (elect()) {
                     const uint32_t o1 = tmem + K::T_O1 + ob * 64;
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < A / 16; ++kk) {
                         const uint64_t x = dx + o + ((kk >> 2) * 512 + (kk & 3) * 2);
                         tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, x, id_o1, kk > 0);
@@ -442,11 +457,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
             }
-            if (!wait(&bars.y_ready[n & 1], n >> 1)) break;
+            if (!wait_all(&bars.y_ready[n & 1], n >> 1)) break;
             tc::tc_fence_after();
-            if (leader) {  // S^T += Z^T Yw
+            if (elect()) {  // S^T += Z^T Yw
                 const uint64_t yw = dw + (uint64_t)((n & 1) * (2 * K::XB >> 4));
-#pragma unroll 1
+#pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + kk * 128, id_s, OUT || n > 0 || kk > 0);
                     tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + ((K::XB >> 4) + kk * 128), id_s, 1u);
@@ -454,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::mma_commit(&bars.d2done);
                 tc::mma_commit(&bars.y_free[n & 1]);
             }
-            if (leader) tc::mma_commit(&bars.free_s[st]);
+            if (elect()) tc::mma_commit(&bars.free_s[st]);
             __syncwarp();
             if (OUT) next(at);
             if (++st == NS) {
@@ -463,18 +478,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         // nothing of this CTA's is in flight when it exits (bounded)
-        if (leader) tc::mma_commit(&bars.drain[0]);
+        if (elect()) tc::mma_commit(&bars.drain[0]);
         __syncwarp();
         tc::mbar_wait(&bars.drain[0], 0, budget / 4);
     } else if (OUT && warp == W_INTRA) {
         constexpr uint32_t id_p = tc::idesc_bf16(64, 64, false, false), id_o2 = tc::idesc_bf16(B, 64, true, false);
         const uint64_t dx = tc::sdesc(sb + K::OFF_X, 16, 1024), dy = tc::sdesc(sb + K::OFF_Y, 16, 1024);
         const uint64_t dz = tc::sdesc(sb + K::OFF_Z, 8192, 1024), dp = tc::sdesc(sb + K::OFF_P, 16, 1024);
-        const bool leader = elect();
         auto issue_p = [&](int n, int st) {  // P = X Y^T
-            if (leader) {
+            if (elect()) {
                 const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-#pragma unroll 1
+#pragma unroll
                 for (int kk = 0; kk < A / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * 512 + (kk & 3) * 2;
                     tc::mma_bf16(tmem + K::T_P + (n & 1) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
@@ -491,16 +505,16 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++ph;
             }
             if (n + 1 < cnt) {
-                if (!wait(&bars.full[st], ph)) break;
+                if (!wait_all(&bars.full[st], ph)) break;
                 tc::tc_fence_after();
                 issue_p(n + 1, st);
             }
             if (n < 0) continue;
-            if (!wait(&bars.p_ready, n) || (n > 0 && !wait(&bars.o_free[(n - 1) & 1], (n - 1) >> 1))) break;
+            if (!wait_all(&bars.p_ready, n) || (n > 0 && !wait_all(&bars.o_free[(n - 1) & 1], (n - 1) >> 1))) break;
             tc::tc_fence_after();
-            if (leader) {  // O2^T = Z^T (D o P)^T
+            if (elect()) {  // O2^T = Z^T (D o P)^T
                 const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));
-#pragma unroll 1
+#pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     tc::mma_bf16(tmem + K::T_O2, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
                 tc::mma_commit(&bars.o2done);
@@ -509,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
         }
-        if (leader) tc::mma_commit(&bars.drain[1]);
+        if (elect()) tc::mma_commit(&bars.drain[1]);
         __syncwarp();
         tc::mbar_wait(&bars.drain[1], 0, budget / 4);
     } else if (warp == W_GATE) {
