@@ -76,7 +76,7 @@ cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, const Segm
 
 // Tensor-core walks (decay_tc.cu): bf16 inputs, a and b of 64 or 128, x, y and z 16-byte aligned.  bwd: walks
 // with dots, given as DOT_PLANES shares (one for each warp of the output group); outputs are bf16.
-// All walks (of the same head sizes) one after another, head by head, are one row of chunks, and each of g CTAs
+// All walks (of the same head sizes) one after another, kind by kind, are one row of chunks, and each of g CTAs
 // takes an even share of it: the end of one walk, whole ones, the start of another.  The stretch of a share
 // that does not end its sequence is the last one; the first pass takes it in `fine` parts.
 constexpr int DOT_PLANES = 4;

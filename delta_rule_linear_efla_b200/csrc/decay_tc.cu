@@ -278,7 +278,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     __shared__ volatile int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wg = warp >> 2, gtid = tid & 127;
-    // ---- this CTA's chunks, [p0, p1) of the row of all walks' chunks, or a part of such a share's last stretch
+    // ---- walks in the order of their kind, then their head: the shares of two kinds that read the same tensors in
+    // the same direction lie alike, so that the later of two readers finds its tiles in L2.
+    // This CTA's chunks, [p0, p1) of the row of all walks' chunks, or a part of such a share's last stretch
     const int NC = (L + C - 1) / C;
     const int share = OUT ? blockIdx.x : blockIdx.x / sh.fine;
     auto bound = [&](int c) { return c * sh.size + min(c, sh.more); };
@@ -288,10 +290,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     struct Place {
         int wi, bh, k;
         bool rev;
-        __device__ __forceinline__ void walk(int n, uint32_t revs) {  // on to the next walk
-            if (++wi == n) {
-                wi = 0;
-                ++bh;
+        __device__ __forceinline__ void walk(int n, uint32_t revs) {  // on to the next walk, n heads of each kind
+            if (++bh == n) {
+                bh = 0;
+                ++wi;
             }
             rev = revs >> wi & 1;
         }
@@ -310,8 +312,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             p0 = (long long)u * NC + at.k;
             p1 = len > 0 ? min(p1, p0 + part) : p0;
         }
-        at.bh = u / ws.n;
-        at.wi = u - at.bh * ws.n;
+        at.wi = u / BH;
+        at.bh = u - at.wi * BH;
         at.rev = revs >> at.wi & 1;
     }
     const int cnt = p1 > p0 ? (int)(p1 - p0) : 0;
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!OUT) --p.k;
         else if (++p.k == NC) {
             p.k = 0;
-            p.walk(ws.n, revs);
+            p.walk(BH, revs);
         }
     };
 
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!OUT) pl.k -= skip;
             else {
 #pragma unroll 1
-                for (pl.k += skip; pl.k >= NC; pl.k -= NC) pl.walk(ws.n, revs);
+                for (pl.k += skip; pl.k >= NC; pl.k -= NC) pl.walk(BH, revs);
             }
             const int t = n + gk < cnt ? pl.chunk(NC) * C + tk : L;
             const float lh = g.per_head && t < L ? heads[pl.bh % g.H] : 0.f;
@@ -746,8 +748,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc::tc_fence_after();
                 if (at.k == 0) {  // the end of a walk: its state leaves
                     Place last = at;
-                    last.bh = at.wi > 0 ? at.bh : at.bh - 1;
-                    last.wi = at.wi > 0 ? at.wi - 1 : ws.n - 1;
+                    last.bh = at.bh > 0 ? at.bh - 1 : BH - 1;
+                    last.wi = at.bh > 0 ? at.wi : at.wi - 1;
                     store_state(last);
                     if (n < cnt) load_state(at, 0, 0, 0, 16);
                 }
@@ -898,7 +900,7 @@ Shares tc_shares(int BH, int L, int n) {
     Shares sh{};
     sh.g = (int)units;
     sh.size = NC;
-    const long long g = total / 4 < SMS ? total / 4 : SMS;  // four chunks a share or more
+    const long long g = (total / 4 < SMS ? total / 4 : SMS) / n * n;  // four chunks a share or more, walks alike
     if (g < 2 || total >= 1LL << 31) return sh;
     const double whole = (double)((units + SMS - 1) / SMS * NC), even = (double)total / g;
     if (even + 0.4 * (even < NC ? even : 0.7 * NC) + 6. >= whole) return sh;
