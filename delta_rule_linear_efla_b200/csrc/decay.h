@@ -102,22 +102,5 @@ cudaError_t launch_dlog(const float *dotq, int nq, const float *dotk, int nk, co
 cudaError_t launch_step(const void *q, const void *k, const void *v, Gate g, float *S, void *o, int BH, int dk,
                         int dv, bool in_bf16, bool o_bf16, cudaStream_t s);
 
-// Launches a kernel that begins with cudaGridDependencySynchronize(): it is set up while the kernel before
-// it in the stream ends.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t c{};
-    c.gridDim = grid;
-    c.blockDim = dim3(threads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
-}
-
 }  // namespace decay
 }  // namespace efla

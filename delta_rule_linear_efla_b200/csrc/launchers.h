@@ -12,6 +12,23 @@ namespace efla {
 // Host-side count of kernels enqueued by the library (efla_kernel_launches).
 void count_launches(unsigned n);
 
+// Launches a kernel that begins with cudaGridDependencySynchronize(): it is set up while the kernel before
+// it in the stream ends.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // Per-token alpha (fused norm + closed-form coefficient).  is_bf16 selects the
 // element type of k and beta.
 // euler: the coefficient is beta (the delta rule's explicit Euler step) instead of the exact flow's.

@@ -18,7 +18,7 @@ namespace norms {
 namespace {
 
 constexpr int NT = 256;
-constexpr int MAX_CTAS = 148 * 8;  // of the kernels that sum a weight gradient
+constexpr int MAX_CTAS = 148 * 8;
 
 template <typename T, int VEC> struct Piece;
 template <> struct Piece<__nv_bfloat16, 8> { using V = uint4; };
@@ -27,13 +27,19 @@ template <> struct Piece<__nv_bfloat16, 4> { using V = uint2; };
 template <> struct Piece<float, 1> { using V = uint32_t; };
 template <> struct Piece<__nv_bfloat16, 1> { using V = uint16_t; };
 
+// A piece as it was loaded; zeros where there is none.
 template <typename T, int VEC>
-__device__ __forceinline__ void ld(float (&f)[VEC], const T *p) {
-    const typename Piece<T, VEC>::V u = *reinterpret_cast<const typename Piece<T, VEC>::V *>(p);
-    const T *h = reinterpret_cast<const T *>(&u);
+struct Raw {
+    typename Piece<T, VEC>::V u;
+    __device__ __forceinline__ void load(const T *p, bool on) {
+        u = on ? *reinterpret_cast<const typename Piece<T, VEC>::V *>(p) : typename Piece<T, VEC>::V{};
+    }
+    __device__ __forceinline__ void to(float (&f)[VEC]) const {
+        const T *h = reinterpret_cast<const T *>(&u);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = to_f32(h[i]);
-}
+        for (int i = 0; i < VEC; ++i) f[i] = to_f32(h[i]);
+    }
+};
 template <typename T, int VEC>
 __device__ __forceinline__ void st(T *p, const float (&f)[VEC]) {
     typename Piece<T, VEC>::V u;
@@ -55,14 +61,18 @@ __device__ __forceinline__ float weight_at(const Weight &w, int i) {
     return w.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(w.p)[i]) : static_cast<const float *>(w.p)[i];
 }
 
+__device__ __forceinline__ unsigned div(unsigned n, const Div &d) {
+    return (unsigned)(((unsigned long long)__umulhi(n, d.mul) + n) >> d.shift);
+}
+
 // Where row r = (b L + t) H + h lies: in the view's strides, and in the kernels' layout [B,H,L,d].
 struct Row {
-    int b, t, h;
-    __device__ __forceinline__ Row(long long r, const Sizes &n) {
-        const long long bt = r / n.H;
-        h = (int)(r - bt * n.H);
-        b = (int)(bt / n.L);
-        t = (int)(bt - (long long)b * n.L);
+    unsigned b, t, h;
+    __device__ __forceinline__ Row(unsigned r, const Sizes &n) {
+        const unsigned bt = div(r, n.byH);
+        h = r - bt * n.H;
+        b = div(bt, n.byL);
+        t = bt - b * n.L;
     }
     __device__ __forceinline__ size_t at(const View &v) const { return b * v.sb + t * v.sl + h * v.sh; }
     __device__ __forceinline__ size_t heads(const Sizes &n) const {
@@ -93,17 +103,22 @@ __device__ __forceinline__ void store_dw(float (&acc)[NV][VEC], float *part, int
     }
 }
 
-// dw[i] = sum of the CTAs' shares, in their order: 32 columns a CTA, 32 rows of threads.
+// dw[i] = sum of the CTAs' shares, in a fixed order: eight columns a CTA, 128 threads a column.
 template <typename TW>
 __global__ void __launch_bounds__(1024) sum_dw_kernel(const float *__restrict__ part, TW *__restrict__ dw, int rows, int d) {
-    __shared__ float red[32][33];
-    const int c = threadIdx.x & 31, g = threadIdx.x >> 5, i = blockIdx.x * 32 + c;
+    __shared__ float red[32][8];
+    cudaGridDependencySynchronize();
+    const int c = threadIdx.x & 7, g = threadIdx.x >> 3, i = blockIdx.x * 8 + c;
     float x = 0.f;
-    if (i < d)
-        for (int r = g; r < rows; r += 32) x += part[(size_t)r * d + i];
-    red[g][c] = x;
+    if (i < d) {
+#pragma unroll 5
+        for (int r = g; r < rows; r += 128) x += part[(size_t)r * d + i];
+    }
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    x += __shfl_xor_sync(0xffffffffu, x, 16);
+    if ((threadIdx.x & 31) < 8) red[threadIdx.x >> 5][c] = x;
     __syncthreads();
-    if (g == 0 && i < d) {
+    if (threadIdx.x < 8 && i < d) {
         float s = 0.f;
 #pragma unroll
         for (int r = 0; r < 32; ++r) s += red[r][c];
@@ -111,104 +126,124 @@ __global__ void __launch_bounds__(1024) sum_dw_kernel(const float *__restrict__ 
     }
 }
 
-// ------------------------------------------------------------------ head norm
-template <typename T, int VEC, int NV, int G>
-__global__ void __launch_bounds__(NT)
-    head_norm_kernel(const View x, const Weight w, T *__restrict__ y, const Sizes n, float m, float scale, float eps) {
-    const int lane = threadIdx.x & 31, gl = lane % G;
-    constexpr int RPC = NT / G;
-    const long long rows = (long long)n.B * n.L * n.H, step = (long long)gridDim.x * RPC;
-    float wv[NV][VEC];
+// Every kernel takes R rows a group at once: their loads are all on the way before the first is used.  Rows of
+// one turn are neighbours (group g of a warp or block takes g, g + groups, ...), turns are a grid apart.
+template <int VEC, int NV, int G>
+struct Group {
+    static constexpr int RPC = NT / G;  // rows of a block at once
+    int gl;
+    __device__ __forceinline__ Group() : gl(threadIdx.x % G) {}
+    __device__ __forceinline__ int at(int j) const { return (j * G + gl) * VEC; }
+    __device__ __forceinline__ void weights(float (&wv)[NV][VEC], const Weight &w, int d, float scale) const {
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int i = (j * G + gl) * VEC + e;
-            wv[j][e] = i < n.d ? scale * weight_at(w, i) : 0.f;
-        }
-    for (long long r0 = (long long)blockIdx.x * RPC; r0 < rows; r0 += step) {
-        const long long r = r0 + threadIdx.x / G;
-        const bool on = r < rows;
-        const Row row(on ? r : 0, n);
-        const T *px = static_cast<const T *>(x.p) + row.at(x);
-        float f[NV][VEC], sum = 0.f;
+            for (int e = 0; e < VEC; ++e) wv[j][e] = at(j) + e < d ? scale * weight_at(w, at(j) + e) : 0.f;
+    }
+    template <typename T>
+    __device__ __forceinline__ void load(Raw<T, VEC> (&f)[NV], const T *p, int d, bool on) const {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
-            if (on && i < n.d) ld<T, VEC>(f[j], px + i);
-            else
+        for (int j = 0; j < NV; ++j) f[j].load(p + at(j), on && at(j) < d);
+    }
+    template <typename T>
+    __device__ __forceinline__ static void to(float (&f)[NV][VEC], const Raw<T, VEC> (&r)[NV]) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) f[j][e] = 0.f;
+        for (int j = 0; j < NV; ++j) r[j].to(f[j]);
+    }
+    template <typename T>
+    __device__ __forceinline__ void store(T *p, const float (&f)[NV][VEC], int d, bool on) const {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (on && at(j) < d) st<T, VEC>(p + at(j), f[j]);
+    }
+    __device__ __forceinline__ float norm(const float (&f)[NV][VEC], float m, float eps) const {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) sum = fmaf(f[j][e], f[j][e], sum);
+        return rsqrtf(fmaf(m, group_sum<G>(sum), eps));
+    }
+};
+
+// ------------------------------------------------------------------ head norm
+template <typename T, int VEC, int NV, int G, int R>
+__global__ void __launch_bounds__(NT, 4)
+    head_norm_kernel(const View x, const Weight w, T *__restrict__ y, const Sizes n, unsigned rows, float m, float scale, float eps) {
+    const Group<VEC, NV, G> g;
+    constexpr unsigned RPC = NT / G;
+    float wv[NV][VEC];
+    g.weights(wv, w, n.d, scale);
+    for (unsigned r0 = blockIdx.x * RPC * R + threadIdx.x / G; r0 - threadIdx.x / G < rows; r0 += gridDim.x * RPC * R) {
+        Raw<T, VEC> xr[R][NV];
+        size_t out[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const unsigned r = r0 + k * RPC;
+            const Row row(r < rows ? r : 0, n);
+            g.load(xr[k], static_cast<const T *>(x.p) + row.at(x), n.d, r < rows);
+            out[k] = row.heads(n);
         }
-        const float rs = rsqrtf(fmaf(m, group_sum<G>(sum), eps));
-        T *py = y + row.heads(n);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
+        for (int k = 0; k < R; ++k) {
+            float f[NV][VEC];
+            g.to(f, xr[k]);
+            const float rs = g.norm(f, m, eps);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) f[j][e] = f[j][e] * rs * wv[j][e];
-            if (on && i < n.d) st<T, VEC>(py + i, f[j]);
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[j][e] = f[j][e] * rs * wv[j][e];
+            g.store(y + out[k], f, n.d, r0 + k * RPC < rows);
         }
     }
 }
 
-template <typename T, int VEC, int NV, int G>
-__global__ void __launch_bounds__(NT)
+template <typename T, int VEC, int NV, int G, int R>
+__global__ void __launch_bounds__(NT, 4)
     head_norm_bwd_kernel(const View x, const Weight w, const T *__restrict__ dy, T *__restrict__ dx,
-                         float *__restrict__ part, const Sizes n, float m, float scale, float eps) {
-    const int lane = threadIdx.x & 31, gl = lane % G;
-    constexpr int RPC = NT / G;
-    const long long rows = (long long)n.B * n.L * n.H, step = (long long)gridDim.x * RPC;
+                         float *__restrict__ part, const Sizes n, unsigned rows, float m, float scale, float eps) {
+    const Group<VEC, NV, G> g;
+    constexpr unsigned RPC = NT / G;
     float wv[NV][VEC], acc[NV][VEC];
+    g.weights(wv, w, n.d, scale);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int i = (j * G + gl) * VEC + e;
-            wv[j][e] = i < n.d ? scale * weight_at(w, i) : 0.f;
-            acc[j][e] = 0.f;
+        for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+    for (unsigned r0 = blockIdx.x * RPC * R + threadIdx.x / G; r0 - threadIdx.x / G < rows; r0 += gridDim.x * RPC * R) {
+        Raw<T, VEC> xr[R][NV], dr[R][NV];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const unsigned r = r0 + k * RPC;
+            const Row row(r < rows ? r : 0, n);
+            g.load(xr[k], static_cast<const T *>(x.p) + row.at(x), n.d, r < rows);
+            g.load(dr[k], dy + row.heads(n), n.d, r < rows);
         }
-    for (long long r0 = (long long)blockIdx.x * RPC; r0 < rows; r0 += step) {
-        const long long r = r0 + threadIdx.x / G;
-        const bool on = r < rows;
-        const Row row(on ? r : 0, n);
-        const T *px = static_cast<const T *>(x.p) + row.at(x);
-        const T *pd = dy + row.heads(n);
-        float f[NV][VEC], gd[NV][VEC], sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
-            if (on && i < n.d) {
-                ld<T, VEC>(f[j], px + i);
-                ld<T, VEC>(gd[j], pd + i);
-            } else {
+        for (int k = 0; k < R; ++k) {
+            const unsigned r = r0 + k * RPC;
+            float f[1][NV][VEC], gd[1][NV][VEC];
+            g.to(f[0], xr[k]);
+            g.to(gd[0], dr[k]);
+            const float rs = g.norm(f[0], m, eps);
+            float dot = 0.f;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) f[j][e] = gd[j][e] = 0.f;
-            }
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum = fmaf(f[j][e], f[j][e], sum);
-        }
-        const float rs = rsqrtf(fmaf(m, group_sum<G>(sum), eps));
-        float dot = 0.f;
+                for (int e = 0; e < VEC; ++e) {
+                    const float nn = f[0][j][e] * rs;
+                    if (r < rows) acc[j][e] = fmaf(gd[0][j][e], nn, acc[j][e]);
+                    const float dn = gd[0][j][e] * wv[j][e];
+                    dot = fmaf(dn, nn, dot);
+                    f[0][j][e] = nn;
+                    gd[0][j][e] = dn;
+                }
+            dot = m * group_sum<G>(dot);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                f[j][e] *= rs;  // n
-                if (on) acc[j][e] = fmaf(gd[j][e], f[j][e], acc[j][e]);
-                gd[j][e] *= wv[j][e];  // dn
-                dot = fmaf(gd[j][e], f[j][e], dot);
-            }
-        dot = m * group_sum<G>(dot);
-        T *po = dx + (size_t)(on ? r : 0) * n.d;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) f[j][e] = rs * fmaf(-dot, f[j][e], gd[j][e]);
-            if (on && i < n.d) st<T, VEC>(po + i, f[j]);
+                for (int e = 0; e < VEC; ++e) f[0][j][e] = rs * fmaf(-dot, f[0][j][e], gd[0][j][e]);
+            g.store(dx + (size_t)r * n.d, f[0], n.d, r < rows);
         }
     }
     if (part) {
@@ -216,129 +251,118 @@ __global__ void __launch_bounds__(NT)
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) acc[j][e] *= scale;
-        store_dw<VEC, NV, G>(acc, part, n.d, lane);
+        store_dw<VEC, NV, G>(acc, part, n.d, threadIdx.x & 31);
     }
 }
 
 // ------------------------------------------------------------------ gated norm
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// 1 / (1 + e^-x).  With bf16 gates the fast exponential and division, a few ulp off: far below the rounding of
+// anything that is made from it (and 0 below -87, where e^-x leaves the division's range).
+template <bool ACCURATE>
+__device__ __forceinline__ float sigmoid_of(float x) {
+    if constexpr (ACCURATE) return 1.f / (1.f + expf(-x));
+    else return x < -87.f ? 0.f : __fdividef(1.f, 1.f + __expf(-x));
+}
 
-template <typename T, typename TO, int VEC, int NV, int G>
-__global__ void __launch_bounds__(NT)
+template <typename T, typename TO, int VEC, int NV, int G, int R>
+__global__ void __launch_bounds__(NT, 4)
     gated_norm_kernel(const TO *__restrict__ o, const View gate, const Weight w, const View res, T *__restrict__ y,
-                      const Sizes n, bool silu, float scale, float eps) {
-    const int lane = threadIdx.x & 31, gl = lane % G;
-    constexpr int RPC = NT / G;
-    const long long rows = (long long)n.B * n.L * n.H, step = (long long)gridDim.x * RPC;
+                      const Sizes n, unsigned rows, bool silu, float scale, float eps) {
+    constexpr bool ACC = sizeof(T) == 4;
+    const Group<VEC, NV, G> g;
+    constexpr unsigned RPC = NT / G;
     const float m = 1.f / n.d;
     float wv[NV][VEC];
+    g.weights(wv, w, n.d, scale);
+    for (unsigned r0 = blockIdx.x * RPC * R + threadIdx.x / G; r0 - threadIdx.x / G < rows; r0 += gridDim.x * RPC * R) {
+        Raw<TO, VEC> fr[R][NV];
+        Raw<T, VEC> gr[R][NV], rr[R][NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int i = (j * G + gl) * VEC + e;
-            wv[j][e] = i < n.d ? scale * weight_at(w, i) : 0.f;
+        for (int k = 0; k < R; ++k) {
+            const unsigned r = r0 + k * RPC;
+            const Row row(r < rows ? r : 0, n);
+            g.load(fr[k], o + row.heads(n), n.d, r < rows);
+            g.load(gr[k], static_cast<const T *>(gate.p) + row.at(gate), n.d, r < rows);
+            g.load(rr[k], static_cast<const T *>(res.p) + row.at(res), n.d, res.p && r < rows);
         }
-    for (long long r0 = (long long)blockIdx.x * RPC; r0 < rows; r0 += step) {
-        const long long r = r0 + threadIdx.x / G;
-        const bool on = r < rows;
-        const Row row(on ? r : 0, n);
-        const TO *po = o + row.heads(n);
-        const T *pg = static_cast<const T *>(gate.p) + row.at(gate);
-        const T *pr = res.p ? static_cast<const T *>(res.p) + row.at(res) : nullptr;
-        float f[NV][VEC], gv[NV][VEC], rv[NV][VEC], sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
+        for (int k = 0; k < R; ++k) {
+            const unsigned r = r0 + k * RPC;
+            float f[1][NV][VEC], gv[1][NV][VEC], rv[1][NV][VEC];
+            g.to(f[0], fr[k]);
+            g.to(gv[0], gr[k]);
+            g.to(rv[0], rr[k]);
+            const float rs = g.norm(f[0], m, eps);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) f[j][e] = gv[j][e] = rv[j][e] = 0.f;
-            if (on && i < n.d) {
-                ld<TO, VEC>(f[j], po + i);
-                ld<T, VEC>(gv[j], pg + i);
-                if (pr) ld<T, VEC>(rv[j], pr + i);
-            }
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum = fmaf(f[j][e], f[j][e], sum);
-        }
-        const float rs = rsqrtf(fmaf(m, group_sum<G>(sum), eps));
-        T *py = y + (size_t)(on ? r : 0) * n.d;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float sg = sigmoid(gv[j][e]), a = silu ? gv[j][e] * sg : sg;
-                f[j][e] = fmaf(f[j][e] * rs * wv[j][e], a, rv[j][e]);
-            }
-            if (on && i < n.d) st<T, VEC>(py + i, f[j]);
+                for (int e = 0; e < VEC; ++e) {
+                    const float sg = sigmoid_of<ACC>(gv[0][j][e]), a = silu ? gv[0][j][e] * sg : sg;
+                    f[0][j][e] = fmaf(f[0][j][e] * rs * wv[j][e], a, rv[0][j][e]);
+                }
+            g.store(y + (size_t)r * n.d, f[0], n.d, r < rows);
         }
     }
 }
 
-template <typename T, typename TO, int VEC, int NV, int G>
-__global__ void __launch_bounds__(NT)
+template <typename T, typename TO, int VEC, int NV, int G, int R>
+__global__ void __launch_bounds__(NT, 4)
     gated_norm_bwd_kernel(const TO *__restrict__ o, const View gate, const Weight w, const T *__restrict__ dy,
                           TO *__restrict__ d_o, T *__restrict__ dgate, float *__restrict__ part, const Sizes n,
-                          bool silu, float scale, float eps) {
-    const int lane = threadIdx.x & 31, gl = lane % G;
-    constexpr int RPC = NT / G;
-    const long long rows = (long long)n.B * n.L * n.H, step = (long long)gridDim.x * RPC;
+                          unsigned rows, bool silu, float scale, float eps) {
+    constexpr bool ACC = sizeof(T) == 4;
+    const Group<VEC, NV, G> g;
+    constexpr unsigned RPC = NT / G;
     const float m = 1.f / n.d;
     float wv[NV][VEC], acc[NV][VEC];
+    g.weights(wv, w, n.d, scale);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int i = (j * G + gl) * VEC + e;
-            wv[j][e] = i < n.d ? scale * weight_at(w, i) : 0.f;
-            acc[j][e] = 0.f;
+        for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
+    for (unsigned r0 = blockIdx.x * RPC * R + threadIdx.x / G; r0 - threadIdx.x / G < rows; r0 += gridDim.x * RPC * R) {
+        Raw<TO, VEC> fr[R][NV];
+        Raw<T, VEC> gr[R][NV], dr[R][NV];
+        size_t at_o[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const unsigned r = r0 + k * RPC;
+            const Row row(r < rows ? r : 0, n);
+            at_o[k] = row.heads(n);
+            g.load(fr[k], o + at_o[k], n.d, r < rows);
+            g.load(gr[k], static_cast<const T *>(gate.p) + row.at(gate), n.d, r < rows);
+            g.load(dr[k], dy + (size_t)r * n.d, n.d, r < rows);
         }
-    for (long long r0 = (long long)blockIdx.x * RPC; r0 < rows; r0 += step) {
-        const long long r = r0 + threadIdx.x / G;
-        const bool on = r < rows;
-        const Row row(on ? r : 0, n);
-        const size_t at_o = row.heads(n), at_y = (size_t)(on ? r : 0) * n.d;
-        const T *pg = static_cast<const T *>(gate.p) + row.at(gate);
-        float f[NV][VEC], gv[NV][VEC], gd[NV][VEC], sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
+        for (int k = 0; k < R; ++k) {
+            const unsigned r = r0 + k * RPC;
+            float f[1][NV][VEC], gv[1][NV][VEC], gd[1][NV][VEC];
+            g.to(f[0], fr[k]);
+            g.to(gv[0], gr[k]);
+            g.to(gd[0], dr[k]);
+            const float rs = g.norm(f[0], m, eps);
+            float dot = 0.f;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) f[j][e] = gv[j][e] = gd[j][e] = 0.f;
-            if (on && i < n.d) {
-                ld<TO, VEC>(f[j], o + at_o + i);
-                ld<T, VEC>(gv[j], pg + i);
-                ld<T, VEC>(gd[j], dy + at_y + i);
-            }
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) sum = fmaf(f[j][e], f[j][e], sum);
-        }
-        const float rs = rsqrtf(fmaf(m, group_sum<G>(sum), eps));
-        float dot = 0.f;
+                for (int e = 0; e < VEC; ++e) {
+                    const float x = gv[0][j][e], sg = sigmoid_of<ACC>(x);
+                    const float a = silu ? x * sg : sg, da = silu ? sg * fmaf(x, 1.f - sg, 1.f) : sg * (1.f - sg);
+                    const float nn = f[0][j][e] * rs, dyv = gd[0][j][e];
+                    if (r < rows) acc[j][e] = fmaf(dyv * a, nn, acc[j][e]);
+                    const float dyw = dyv * wv[j][e];
+                    gv[0][j][e] = dyw * nn * da;  // dgate
+                    gd[0][j][e] = dyw * a;        // dn
+                    f[0][j][e] = nn;
+                    dot = fmaf(gd[0][j][e], nn, dot);
+                }
+            dot = m * group_sum<G>(dot);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const float x = gv[j][e], sg = sigmoid(x);
-                const float a = silu ? x * sg : sg, da = silu ? sg * fmaf(x, 1.f - sg, 1.f) : sg * (1.f - sg);
-                const float nn = f[j][e] * rs, dyv = gd[j][e];
-                if (on) acc[j][e] = fmaf(dyv * a, nn, acc[j][e]);
-                const float dyw = dyv * wv[j][e];
-                gv[j][e] = dyw * nn * da;  // dgate
-                gd[j][e] = dyw * a;        // dn
-                f[j][e] = nn;
-                dot = fmaf(gd[j][e], nn, dot);
-            }
-        dot = m * group_sum<G>(dot);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int i = (j * G + gl) * VEC;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) f[j][e] = rs * fmaf(-dot, f[j][e], gd[j][e]);
-            if (on && i < n.d) {
-                st<TO, VEC>(d_o + at_o + i, f[j]);
-                st<T, VEC>(dgate + at_y + i, gv[j]);
-            }
+                for (int e = 0; e < VEC; ++e) f[0][j][e] = rs * fmaf(-dot, f[0][j][e], gd[0][j][e]);
+            g.store(d_o + at_o[k], f[0], n.d, r < rows);
+            g.store(dgate + (size_t)r * n.d, gv[0], n.d, r < rows);
         }
     }
     if (part) {
@@ -346,7 +370,7 @@ __global__ void __launch_bounds__(NT)
         for (int j = 0; j < NV; ++j)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) acc[j][e] *= scale;
-        store_dw<VEC, NV, G>(acc, part, n.d, lane);
+        store_dw<VEC, NV, G>(acc, part, n.d, threadIdx.x & 31);
     }
 }
 
@@ -374,24 +398,29 @@ cudaError_t by_width(int d, F f) {
     }
 }
 
-unsigned grid_for(const Sizes &n, int G, int most) {
-    const long long rows = (long long)n.B * n.L * n.H, rpc = NT / G, want = (rows + rpc - 1) / rpc;
-    return (unsigned)(want < most ? want : most);
+// Blocks of R rows a group: at most eight a processor, which then take turns.
+unsigned grid_for(const Sizes &n, int G, int R) {
+    const long long rpc = (long long)(NT / G) * R, want = (n.rows() + rpc - 1) / rpc;
+    return (unsigned)(want < MAX_CTAS ? want : MAX_CTAS);
 }
+// Rows at once: as many as keep a thread's pieces in registers; one where there are few (the blocks then spread).
+template <int NV> constexpr int rows_at_once(int tensors) { return NV > 1 || tensors > 2 ? 1 : tensors == 1 ? 4 : 2; }
+bool few(const Sizes &n, int G) { return n.rows() < (long long)(NT / G) * MAX_CTAS; }
 
 cudaError_t finish_dw(void *dw, bool w_bf16, const float *ws, int rows, int d, cudaStream_t s) {
-    const unsigned blocks = (d + 31) / 32;
-    if (w_bf16) sum_dw_kernel<<<blocks, 1024, 0, s>>>(ws, (__nv_bfloat16 *)dw, rows, d);
-    else sum_dw_kernel<<<blocks, 1024, 0, s>>>(ws, (float *)dw, rows, d);
+    const unsigned blocks = (d + 7) / 8;
     count_launches(1);
-    return cudaGetLastError();
+    if (w_bf16) return launch_after(sum_dw_kernel<__nv_bfloat16>, dim3(blocks), 1024, 0, s, ws, (__nv_bfloat16 *)dw, rows, d);
+    return launch_after(sum_dw_kernel<float>, dim3(blocks), 1024, 0, s, ws, (float *)dw, rows, d);
 }
 
 template <typename T, int VEC>
 cudaError_t head_fwd(View x, Weight w, void *y, Sizes n, float m, float scale, float eps, cudaStream_t s) {
     return by_width<VEC>(n.d, [&](auto vec, auto nv, auto g) {
         constexpr int V = decltype(vec)::value, N = decltype(nv)::value, G = decltype(g)::value;
-        head_norm_kernel<T, V, N, G><<<grid_for(n, G, 1 << 30), NT, 0, s>>>(x, w, (T *)y, n, m, scale, eps);
+        constexpr int R = rows_at_once<N>(1);
+        if (few(n, G)) head_norm_kernel<T, V, N, G, 1><<<grid_for(n, G, 1), NT, 0, s>>>(x, w, (T *)y, n, (unsigned)n.rows(), m, scale, eps);
+        else head_norm_kernel<T, V, N, G, R><<<grid_for(n, G, R), NT, 0, s>>>(x, w, (T *)y, n, (unsigned)n.rows(), m, scale, eps);
         count_launches(1);
         return cudaGetLastError();
     });
@@ -401,8 +430,11 @@ cudaError_t head_bwd(View x, Weight w, const void *dy, void *dx, void *dw, Sizes
                      float *ws, cudaStream_t s) {
     return by_width<VEC>(n.d, [&](auto vec, auto nv, auto g) {
         constexpr int V = decltype(vec)::value, N = decltype(nv)::value, G = decltype(g)::value;
-        const unsigned grid = grid_for(n, G, MAX_CTAS);
-        head_norm_bwd_kernel<T, V, N, G><<<grid, NT, 0, s>>>(x, w, (const T *)dy, (T *)dx, dw ? ws : nullptr, n, m, scale, eps);
+        constexpr int R = rows_at_once<N>(2);
+        const bool one = few(n, G);
+        const unsigned grid = grid_for(n, G, one ? 1 : R);
+        if (one) head_norm_bwd_kernel<T, V, N, G, 1><<<grid, NT, 0, s>>>(x, w, (const T *)dy, (T *)dx, dw ? ws : nullptr, n, (unsigned)n.rows(), m, scale, eps);
+        else head_norm_bwd_kernel<T, V, N, G, R><<<grid, NT, 0, s>>>(x, w, (const T *)dy, (T *)dx, dw ? ws : nullptr, n, (unsigned)n.rows(), m, scale, eps);
         count_launches(1);
         const cudaError_t e = cudaGetLastError();
         return e != cudaSuccess || !dw ? e : finish_dw(dw, w.bf16, ws, grid, n.d, s);
@@ -413,7 +445,9 @@ cudaError_t gated_fwd(const void *o, View gate, Weight w, View res, void *y, Siz
                       cudaStream_t s) {
     return by_width<VEC>(n.d, [&](auto vec, auto nv, auto g) {
         constexpr int V = decltype(vec)::value, N = decltype(nv)::value, G = decltype(g)::value;
-        gated_norm_kernel<T, TO, V, N, G><<<grid_for(n, G, 1 << 30), NT, 0, s>>>((const TO *)o, gate, w, res, (T *)y, n, silu, scale, eps);
+        constexpr int R = rows_at_once<N>(2);
+        if (few(n, G)) gated_norm_kernel<T, TO, V, N, G, 1><<<grid_for(n, G, 1), NT, 0, s>>>((const TO *)o, gate, w, res, (T *)y, n, (unsigned)n.rows(), silu, scale, eps);
+        else gated_norm_kernel<T, TO, V, N, G, R><<<grid_for(n, G, R), NT, 0, s>>>((const TO *)o, gate, w, res, (T *)y, n, (unsigned)n.rows(), silu, scale, eps);
         count_launches(1);
         return cudaGetLastError();
     });
@@ -423,9 +457,12 @@ cudaError_t gated_bwd(const void *o, View gate, Weight w, const void *dy, void *
                       bool silu, float scale, float eps, float *ws, cudaStream_t s) {
     return by_width<VEC>(n.d, [&](auto vec, auto nv, auto g) {
         constexpr int V = decltype(vec)::value, N = decltype(nv)::value, G = decltype(g)::value;
-        const unsigned grid = grid_for(n, G, MAX_CTAS);
-        gated_norm_bwd_kernel<T, TO, V, N, G><<<grid, NT, 0, s>>>((const TO *)o, gate, w, (const T *)dy, (TO *)d_o,
-                                                                  (T *)dgate, dw ? ws : nullptr, n, silu, scale, eps);
+        constexpr int R = rows_at_once<N>(3);
+        const bool one = few(n, G);
+        const unsigned grid = grid_for(n, G, one ? 1 : R);
+        auto *kernel = one ? gated_norm_bwd_kernel<T, TO, V, N, G, 1> : gated_norm_bwd_kernel<T, TO, V, N, G, R>;
+        kernel<<<grid, NT, 0, s>>>((const TO *)o, gate, w, (const T *)dy, (TO *)d_o, (T *)dgate, dw ? ws : nullptr, n,
+                                   (unsigned)n.rows(), silu, scale, eps);
         count_launches(1);
         const cudaError_t e = cudaGetLastError();
         return e != cudaSuccess || !dw ? e : finish_dw(dw, w.bf16, ws, grid, n.d, s);

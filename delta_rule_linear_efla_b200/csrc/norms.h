@@ -18,8 +18,21 @@ struct View {
     const void *p;
     long long sb, sl, sh;
 };
+// Division by a number below 2^31 as a multiplication (Granlund and Montgomery): n / d for n < 2^31.
+struct Div {
+    unsigned mul, shift, d;
+    Div() = default;
+    explicit Div(unsigned dd) : d(dd) {
+        shift = 0;
+        while ((1ull << shift) < d) ++shift;
+        mul = (unsigned)(((1ull << 32) * ((1ull << shift) - d)) / d + 1);
+    }
+};
 struct Sizes {
     int B, L, H, d;
+    Div byH, byL;
+    Sizes(int b, int l, int h, int dd) : B(b), L(l), H(h), d(dd), byH(h), byL(l) {}
+    long long rows() const { return (long long)B * L * H; }
 };
 struct Weight {
     const void *p;  // [d], or null for ones

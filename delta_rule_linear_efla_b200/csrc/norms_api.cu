@@ -11,6 +11,8 @@ using efla::norms::Sizes;
 using efla::norms::View;
 using efla::norms::Weight;
 
+constexpr long long MAX_ROWS = 0x7f000000LL;
+
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 size_t elem(efla_dtype dt) { return dt == EFLA_BF16 ? 2 : 4; }
 bool dtype_ok(efla_dtype d) { return d == EFLA_F32 || d == EFLA_BF16; }
@@ -24,8 +26,8 @@ efla_status check(int B, int L, int H, int d, efla_dtype dt, efla_dtype w_dt, co
     if (!option || !(eps >= 0.f) || !isfinite(eps) || !isfinite(scale)) return EFLA_ERR_OPTION;
     if (B < 0 || L < 0 || H < 0 || d < 1) return EFLA_ERR_SHAPE;
     if (d > efla::norms::DMAX) return EFLA_ERR_UNSUPPORTED;
-    // one group of at least four lanes a row, 256 threads a block: below 2^31 blocks
-    if ((long long)B * L > (1LL << 40) || (B && L && (long long)H > (1LL << 33) / ((long long)B * L))) return EFLA_ERR_SHAPE;
+    // rows are counted in 32 bits, a turn past the last one
+    if ((long long)B * L >= MAX_ROWS || (long long)B * L * H >= MAX_ROWS) return EFLA_ERR_SHAPE;
     if (!aligned(w, w ? elem(w_dt) : 1)) return EFLA_ERR_ALIGN;
     return EFLA_OK;
 }

@@ -440,7 +440,7 @@ efla_status efla_decay_recurrent_step(const void *q, const void *k, const void *
  * where dw is given, dw in w_dt, summed in a fixed order through workspace
  * (efla_norm_bwd_workspace_size(d) bytes, 16-byte aligned; unused without dw).  dL/dresidual
  * is dy itself.  Outputs must not alias an input otherwise.
- * Sizes: B,L,H >= 0 (no rows is a no-op; dw is then 0), 1 <= d <= 256.  EFLA_ERR_OPTION: an
+ * Sizes: B,L,H >= 0 (no rows is a no-op; dw is then 0), B*L*H < 0x7f000000, 1 <= d <= 256.  EFLA_ERR_OPTION: an
  * unknown kind or act, or a scale or eps that is not finite, or eps < 0.  A row of zeros with
  * eps = 0 gives NaN.
  */
