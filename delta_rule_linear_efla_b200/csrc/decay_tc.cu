@@ -56,16 +56,18 @@ constexpr int GB = 4, SLOTS = 2 * GB;  // chunks whose decay weights are made at
 constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
 
 struct Maps {
-    CUtensorMap x[MAX_WALKS], y[MAX_WALKS], z[MAX_WALKS];
+    CUtensorMap x[MAX_WALKS], y[MAX_WALKS], z[MAX_WALKS], d[MAX_WALKS];
 };
 
 template <int A, int B, bool BWD>
 struct Cfg {
     static constexpr int XB = (A / 64) * 8192, ZB = (B / 64) * 8192;
     static constexpr int OFF_X = 0, OFF_Y = XB, OFF_Z = 2 * XB, STAGE = 2 * XB + ZB;
-    static constexpr int OFF_W = NS * STAGE;        // Yw: two buffers of [hi | lo]
-    static constexpr int OFF_P = OFF_W + 4 * XB;    // D o P
-    static constexpr int SMEM = OFF_P + 8192 + 1024;  // + alignment slack
+    // Yw: two buffers of its hi half, one of its lo half (written when the product that read the last is done)
+    static constexpr int OFF_W = NS * STAGE, OFF_L = OFF_W + 2 * XB;
+    static constexpr int OFF_P = OFF_L + XB;           // D o P
+    static constexpr int OFF_D = OFF_P + 8192;         // backwards: the dots' other factor, half a chunk for each output group
+    static constexpr int SMEM = OFF_D + (BWD ? ZB : 0) + 1024;  // + alignment slack
     // tensor memory columns
     // P twice, so that the mask's loop does not wait for the next one; O1^T twice where it fits
     static constexpr int NO1 = BWD && A == 128 ? 1 : 2;
@@ -76,14 +78,14 @@ struct Cfg {
 
 struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
-    uint64_t full[NS], gready[2], y_free[2], pdone[2], d2done, o1done[2], o2done, o2read, drain[2];
+    uint64_t full[NS], gready[2], y_free[2], pdone[2], d2done, o1done[2], o2done, o2read, drain[2], dfull[2], l_free;
     // one arrival from each of four warps
     uint64_t p_ready, s_ready;
     uint64_t gfree[2], o_free[2];  // the eight output warps (without output, gfree: the weights' sixteen)
     uint64_t y_ready[2];               // the weights' four warps, sixteen without output
     uint64_t free_s[NS];               // one from each issuer
 };
-constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 1 + 2 + 2 + 2, BARS_FOUR = BARS_ONE + 2,
+constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 1 + 2 + 2 + 2 + 3, BARS_FOUR = BARS_ONE + 2,
               BARS_OUT = BARS_FOUR + 2 + 2, BARS_Y = BARS_OUT + 2;
 
 struct Slot {
@@ -414,6 +416,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     tc::tma_prefetch_4d(&maps.y[far.wi], 0, c0, 0, far.bh);
                     if (OUT) tc::tma_prefetch_4d(&maps.x[far.wi], 0, c0, 0, far.bh);
                     tc::tma_prefetch_4d(&maps.z[far.wi], 0, c0, 0, far.bh);
+                    if (OUT && BWD && ws.w[far.wi].dot) {
+                        tc::tma_prefetch_4d(&maps.d[far.wi], 0, c0, 0, far.bh);
+                        tc::tma_prefetch_4d(&maps.d[far.wi], 0, c0 + C / 2, 0, far.bh);
+                    }
                 }
                 next(far);
             }
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // The whole warp runs the loop and one elected lane issues, so that descriptors are warp-uniform.
         constexpr uint32_t id_s = tc::idesc_bf16(B, A, true, true), id_o1 = tc::idesc_bf16(B, 64, false, false);
         const uint64_t dx = tc::sdesc(sb + K::OFF_X, 16, 1024), dz = tc::sdesc(sb + K::OFF_Z, 8192, 1024);
-        const uint64_t dw = tc::sdesc(sb + K::OFF_W, 8192, 1024);
+        const uint64_t dh = tc::sdesc(sb + K::OFF_W, 8192, 1024), dl = tc::sdesc(sb + K::OFF_L, 8192, 1024);
         int st = 0, ph = 0;  // stage and its pass
         for (int n = 0; n < cnt; ++n) {
             const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool split = BWD && ws.w[at.wi].dot;
                 if (elect()) {
                     const uint32_t o1 = tmem + K::T_O1 + ob * 64;
-#pragma unroll
+#pragma unroll 2
                     for (int kk = 0; kk < A / 16; ++kk) {
                         const uint64_t x = dx + o + ((kk >> 2) * 512 + (kk & 3) * 2);
                         tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, x, id_o1, kk > 0);
@@ -462,14 +468,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!wait_all(&bars.y_ready[n & 1], n >> 1)) break;
             tc::tc_fence_after();
             if (elect()) {  // S^T += Z^T Yw
-                const uint64_t yw = dw + (uint64_t)((n & 1) * (2 * K::XB >> 4));
-#pragma unroll
+                const uint64_t yh = dh + (uint64_t)((n & 1) * (K::XB >> 4));
+#pragma unroll 1
                 for (int kk = 0; kk < 4; ++kk) {
-                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + kk * 128, id_s, OUT || n > 0 || kk > 0);
-                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yw + ((K::XB >> 4) + kk * 128), id_s, 1u);
+                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yh + kk * 128, id_s, OUT || n > 0 || kk > 0);
+                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, dl + kk * 128, id_s, 1u);
                 }
                 tc::mma_commit(&bars.d2done);
                 tc::mma_commit(&bars.y_free[n & 1]);
+                tc::mma_commit(&bars.l_free);
             }
             if (elect()) tc::mma_commit(&bars.free_s[st]);
             __syncwarp();
@@ -490,7 +497,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto issue_p = [&](int n, int st) {  // P = X Y^T
             if (elect()) {
                 const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-#pragma unroll
+#pragma unroll 2
                 for (int kk = 0; kk < A / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * 512 + (kk & 3) * 2;
                     tc::mma_bf16(tmem + K::T_P + (n & 1) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tc_fence_after();
             if (elect()) {  // O2^T = Z^T (D o P)^T
                 const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));
-#pragma unroll
+#pragma unroll 2
                 for (int kk = 0; kk < 4; ++kk)
                     tc::mma_bf16(tmem + K::T_O2, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
                 tc::mma_commit(&bars.o2done);
@@ -533,7 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         // between its token and the chunk's start or end, and each is summed from that side: fp32 rounds a sum
         // by 2^-24 of itself, and where that is much the weight is nothing.
         float sum = 0.f;
-        float x[8];
+        float x[8] = {};
         const int gk = lane >> 3, tk = 8 * (lane & 7);  // this lane's chunk of the four, and its first token in it
         const __nv_bfloat16 *tokens = static_cast<const __nv_bfloat16 *>(g.p);
         const float *heads = static_cast<const float *>(g.p);
@@ -555,8 +562,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (t + i >= L) x[i] = 0.f;
             }
         };
-        load(0, gk);
-        for (int n = 0; n < cnt; n += GB) {
+#pragma unroll 1
+        for (int n = -GB; n < cnt; n += GB) {
             float c[8], d[8];  // sums up to and with the token, and behind it, in units of log 2, of this lane's eight
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -564,7 +571,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 c[i] = l * 1.44269504f;
             }
             rev = pl.rev;
-            if (n + GB < cnt) load(n + GB, GB);
+            if (n + GB < cnt) load(n + GB, n < 0 ? gk : GB);
+            if (n < 0) continue;
             d[7] = 0.f;
 #pragma unroll
             for (int i = 6; i >= 0; --i) d[i] = d[i + 1] + c[i + 1];
@@ -630,23 +638,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int n = 0; n < cnt; ++n) {
             if (!wait_gate(n) || !wait(&bars.full[n % NS], n / NS)) break;
             if (n >= 2 && !wait(&bars.y_free[n & 1], (n >> 1) - 1)) break;
-            const uint4 *y = reinterpret_cast<const uint4 *>(base + (n % NS) * K::STAGE + K::OFF_Y);
-            uint4 *hi = reinterpret_cast<uint4 *>(base + K::OFF_W + (n & 1) * 2 * K::XB);
-            uint4 *lo = hi + K::XB / 16;
+            constexpr int T = OUT ? 128 : 512, PIECES = K::XB / 16 / T;
+            const int i0 = OUT ? gtid : tid;
+            const uint4 *y = reinterpret_cast<const uint4 *>(base + (n % NS) * K::STAGE + K::OFF_Y) + i0;
+            uint4 *hi = reinterpret_cast<uint4 *>(base + K::OFF_W + (n & 1) * K::XB) + i0;
+            uint4 *lo = reinterpret_cast<uint4 *>(base + K::OFF_L) + i0;
             const uint32_t *kw = slots[n % SLOTS].kw;
-#pragma unroll 2
-            for (int i = OUT ? gtid : tid; i < K::XB / 16; i += OUT ? 128 : 512) {  // 8 pieces of 16 bytes a row of a 64-column slab
-                const uint32_t f = kw[(i >> 3) & 63];
+            uint4 l[PIECES];
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {  // 8 pieces of 16 bytes a row of a 64-column slab
+                const uint32_t f = kw[(i0 + i * T) >> 3 & 63];
                 const uint32_t fh = __byte_perm(f, f, 0x1010), fl = __byte_perm(f, f, 0x3232);
-                const uint4 u = y[i];
-                uint4 h, l;
-                weigh(u.x, fh, fl, h.x, l.x);
-                weigh(u.y, fh, fl, h.y, l.y);
-                weigh(u.z, fh, fl, h.z, l.z);
-                weigh(u.w, fh, fl, h.w, l.w);
-                hi[i] = h;
-                lo[i] = l;
+                const uint4 u = y[i * T];
+                uint4 h;
+                weigh(u.x, fh, fl, h.x, l[i].x);
+                weigh(u.y, fh, fl, h.y, l[i].y);
+                weigh(u.z, fh, fl, h.z, l[i].z);
+                weigh(u.w, fh, fl, h.w, l[i].w);
+                hi[i * T] = h;
             }
+            if (n >= 1 && !wait(&bars.l_free, n - 1)) break;
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) lo[i * T] = l[i];
             tc::fence_async_smem();
             warp_arrive(&bars.y_ready[n & 1], lane);
             if (!OUT && lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
@@ -690,7 +703,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             const Slot &sl = slots[n % SLOTS];
             const float ca = sl.c2[r], cb = sl.c2[r + 8];
             const uint32_t tp = tmem + lane_base + K::T_P + (n & 1) * 64;
-            uint32_t u[4][4];  // the diagonal block, and up to three on the on side
+            uint32_t u[4];
+            auto store = [&](int c0) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint32_t *>(pt + tc::sw128_off(r + 8 * e, (c0 >> 3) + k) + 2 * cq) = u[2 * k + e];
+            };
             {
                 float v[8];
                 tmem_ld_16x256(tp + r0, v);
@@ -702,40 +722,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int e = 0; e < 2; ++e) {  // row r + 8 e, columns c and c + 1
                         const float cr = e ? cb : ca;
                         const int a = rev ? c - r - 8 * e : r + 8 * e - c, a1 = rev ? a + 1 : a - 1;  // on where >= 0
-                        u[3][2 * k + e] = tc::pack_bf16(a >= 0 ? v[4 * k + 2 * e] * ex2(cr - cc.x) : 0.f,
-                                                        a1 >= 0 ? v[4 * k + 2 * e + 1] * ex2(cr - cc.y) : 0.f);
-                    }
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < 3; ++b) {
-                const int c0 = on0 + 16 * b;
-                if (c0 < on1) {
-                    float v[8];
-                    tmem_ld_16x256(tp + c0, v);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float ce = sl.c2[c0 + 8 * k + (rev ? 0 : 7)];
-                        const F2 f = *reinterpret_cast<const F2 *>(&sl.gw[c0 + 8 * k + cq]);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = ex2((e ? cb : ca) - ce);
-                            u[b][2 * k + e] = pack(f2(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]) * (f2(x, x) * f));
-                        }
+                        u[2 * k + e] = tc::pack_bf16(a >= 0 ? v[4 * k + 2 * e] * ex2(cr - cc.x) : 0.f,
+                                                     a1 >= 0 ? v[4 * k + 2 * e + 1] * ex2(cr - cc.y) : 0.f);
                     }
                 }
             }
             if (n > 0 && !wait(&bars.o2done, n - 1)) break;  // the tile's last reader
+            store(r0);
+#pragma unroll 1
+            for (int c0 = on0; c0 < on1; c0 += 16) {
+                float v[8];
+                tmem_ld_16x256(tp + c0, v);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int c0 = b == 3 ? r0 : on0 + 16 * b;
-                if (b == 3 || c0 < on1) {
+                for (int k = 0; k < 2; ++k) {
+                    const float ce = sl.c2[c0 + 8 * k + (rev ? 0 : 7)];
+                    const F2 f = *reinterpret_cast<const F2 *>(&sl.gw[c0 + 8 * k + cq]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<uint32_t *>(pt + tc::sw128_off(r + 8 * e, (c0 >> 3) + k) + 2 * cq) = u[b][2 * k + e];
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = ex2((e ? cb : ca) - ce);
+                        u[2 * k + e] = pack(f2(v[4 * k + 2 * e], v[4 * k + 2 * e + 1]) * (f2(x, x) * f));
+                    }
                 }
+                store(c0);
             }
             tc::fence_async_smem();
             warp_arrive(&bars.p_ready, lane);
@@ -783,28 +791,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (OUT && (wg == 3 || wg == 4)) {
         // ---------------------------------------------------------- out
         const int j = acc_row<B>(warp & 3, lane), h0 = wg == 3 ? 0 : 32;  // tokens h0 .. h0 + 31 of a chunk
+        int loads = 0;  // of the dots' other factor: the group's half of a chunk's tile, by its first lane
+        const int half = wg - 3;
+        uint8_t *dt = base + K::OFF_D + half * (K::ZB / 2);
+#pragma unroll 1
         for (int n = 0; n < cnt; ++n) {
-            const int t0 = at.chunk(NC) * C + h0, cl = min(32, L - t0), bh = at.bh;
-            const Walk &w = ws.w[at.wi];
+            const int t0 = at.chunk(NC) * C + h0, cl = min(32, L - t0), bh = at.bh, wi = at.wi;
+            const Walk &w = ws.w[wi];
             const bool split = BWD && w.dot != nullptr;
+            if (split) {  // every lane has read the last one
+                if (gtid == 0) {
+                    tc::mbar_expect_tx(&bars.dfull[half], K::ZB / 2);
+                    tc::tma_load_4d(dt, &maps.d[wi], &bars.dfull[half], 0, t0, 0, bh);
+                }
+                ++loads;
+            }
             const size_t row0 = (size_t)bh * L + t0;
             next(at);
-            uint32_t xr[16];  // this lane's elements of the dots' other factor, two tokens a word
-            if (split) {
-                const unsigned short *dx = static_cast<const unsigned short *>(w.dotx) + row0 * B + j;
-                const int xl = j >= 0 ? cl : 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint32_t a = 2 * i < xl ? dx[2 * i * B] : 0, b = 2 * i + 1 < xl ? dx[(2 * i + 1) * B] : 0;
-                    xr[i] = a | b << 16;
-                }
-                // the next chunk's on their way to L2: a row of this warp's columns a lane
-                const Walk &nw = ws.w[at.wi];
-                const int t = at.chunk(NC) * C + h0 + lane;
-                if (n + 1 < cnt && nw.dot && t < L)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const unsigned short *>(nw.dotx) +
-                                                                  ((size_t)at.bh * L + t) * B + (B / 4) * (warp & 3)));
-            }
             if (!wait_gate(n) || !wait(&bars.o1done[n & 1], n >> 1) || !wait(&bars.o2read, n)) break;
             tc::tc_fence_after();
             const float *qw = slots[n % SLOTS].qw + h0;
@@ -827,24 +830,24 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
             if (j >= 0) {
                 TO *out = static_cast<TO *>(w.out) + row0 * B + j;
-                if (cl == 32) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], true, true);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], i < cl, i + 1 < cl);
-                }
+                for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], i < cl, i + 1 < cl);
             }
             if (split) {
+                if (!wait(&bars.dfull[half], loads - 1)) break;
+                const int c = (j < 0 ? 0 : j) & 63;
+                const uint8_t *x = dt + (j >= 64 ? 4096 : 0) + (c & 7) * 2;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[2 * i] = j >= 0 ? v[2 * i] * bf_lo(xr[i]) : 0.f;
-                    v[2 * i + 1] = j >= 0 ? v[2 * i + 1] * bf_hi(xr[i]) : 0.f;
+                for (int i = 0; i < 32; ++i) {
+                    const uint32_t u = *reinterpret_cast<const unsigned short *>(x + tc::sw128_off(i, c >> 3));
+                    v[i] = B == 128 || j >= 0 ? v[i] * bf_lo(u) : 0.f;
                 }
+                tc::named_bar_sync(2 + half, 128);  // the tile is read
                 const float s = column_sums(v, lane);
                 if (lane < cl) w.dot[((size_t)(warp & 3) * BH + bh) * L + t0 + lane] = s;
             }
         }
+        if (loads > 0) tc::mbar_wait(&bars.dfull[half], (loads - 1) & 1, budget / 8);  // nothing in flight at the end
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -870,7 +873,8 @@ cudaError_t launch_ab(const Walks &ws, Gate g, int BH, int L, const Shares &sh, 
     for (int i = 0; i < ws.n; ++i) {
         const Walk &w = ws.w[i];
         if (!tmap::make_slabs(&maps.x[i], w.x, w.a / 64, L, BH, C) || !tmap::make_slabs(&maps.y[i], w.y, w.a / 64, L, BH, C) ||
-            !tmap::make_slabs(&maps.z[i], w.z, w.b / 64, L, BH, C))
+            !tmap::make_slabs(&maps.z[i], w.z, w.b / 64, L, BH, C) ||
+            (w.dot && !tmap::make_slabs(&maps.d[i], w.dotx, w.b / 64, L, BH, C / 2)))
             return cudaErrorInvalidValue;
     }
     const int a = ws.w[0].a, b = ws.w[0].b;

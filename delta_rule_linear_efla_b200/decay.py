@@ -29,23 +29,34 @@ def _switch(device, stream):
                 yield stream.cuda_stream
 
 
+# The current stream's handle without the Stream object around it (3 us of a decode step's call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _Here:
     """The current device's current stream: nothing to switch."""
 
+    def __init__(self, index: int):
+        self.index = index
+
     def __enter__(self):
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.index) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         return False
 
 
-_here = _Here()
+_here: dict = {}
 
 
 def _launch_on(device, stream):
     """Context in which a call on tensors of `device` allocates and launches; gives the stream's handle."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return _here
+    index = device.index
+    if stream is None and index == torch.cuda.current_device():
+        here = _here.get(index)
+        if here is None:
+            here = _here[index] = _Here(index)
+        return here
     return _switch(device, stream)
 
 
@@ -53,6 +64,8 @@ def _arg(t, name: str, device, shape, dtype) -> int:
     """The address of a dense CUDA tensor of that device, shape and dtype (0 for None)."""
     if t is None:
         return 0
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.device != device:
@@ -116,9 +129,9 @@ def decay_chunk_fwd(q, k, v, log_g, S0=None, o=None, S_final=None, want_state: b
     lib = load_library()
     with _launch_on(device, stream) as s:
         if o is None:
-            o = torch.empty(rows, dtype=o_dtype, device=device)
+            o = q.new_empty(rows, dtype=o_dtype)
         if S_final is None and want_state:
-            S_final = torch.empty(state, dtype=torch.float32, device=device)
+            S_final = q.new_empty(state, dtype=torch.float32)
         ws, have = _workspace(workspace, lib.efla_decay_chunk_fwd_workspace_size(B, H, L, dk, dv, code), device)
         _check(lib.efla_decay_chunk_fwd(qp, kp, vp, gp, form, S0p, _arg(o, "o", device, rows, o_dtype),
                                         _arg(S_final, "S_final", device, state, torch.float32), B, H, L, dk, dv, code,
@@ -143,7 +156,7 @@ def decay_bwd(q, k, v, log_g, dO, S0=None, dS_final=None, want_dS0: bool = True,
     with _launch_on(device, stream) as s:
         dq, dkey, dval = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         dlog = torch.empty_like(log_g) if form == DECAY_TOKEN else None
-        dS0 = torch.empty(state, dtype=torch.float32, device=device) if want_dS0 else None
+        dS0 = q.new_empty(state, dtype=torch.float32) if want_dS0 else None
         ws, have = _workspace(workspace, lib.efla_decay_bwd_workspace_size(B, H, L, dk, dv, code), device)
         _check(lib.efla_decay_bwd(qp, kp, vp, gp, form, S0p, dOp, dSp, dq.data_ptr(), dkey.data_ptr(), dval.data_ptr(),
                                   dlog.data_ptr() if dlog is not None else 0, dS0.data_ptr() if want_dS0 else 0, B, H, L,
@@ -166,7 +179,7 @@ def decay_recurrent_step(q, k, v, log_g, S, o=None, o_dtype=None, stream=None):
     Sp = _arg(S, "S", device, (B, H, dk, dv), torch.float32)
     with _launch_on(device, stream) as s:
         if o is None:
-            o = torch.empty((B, H, dv), dtype=o_dtype, device=device)
+            o = q.new_empty((B, H, dv), dtype=o_dtype)
         _check(load_library().efla_decay_recurrent_step(qp, kp, vp, gp, form, Sp, _arg(o, "o", device, (B, H, dv), o_dtype),
                                                         B, H, dk, dv, code, _code(o_dtype), s), "efla_decay_recurrent_step")
     return o
