@@ -78,15 +78,16 @@ cudaError_t launch_walks_simt(const Walks &ws, Gate g, int BH, int L, const Segm
 // with dots, given as DOT_PLANES shares (one for each warp of the output group); outputs are bf16.
 // All walks (of the same head sizes) one after another, kind by kind, are one row of chunks, and each of g CTAs
 // takes an even share of it: the end of one walk, whole ones, the start of another.  The stretch of a share
-// that does not end its sequence is the last one; the first pass takes it in `fine` parts.
+// that does not end its sequence is the last one.
 constexpr int DOT_PLANES = 4;
 struct Shares {
-    int g, fine;
-    long long size;  // chunks in a share; the first `more` have one more
+    int g;
+    bool cut;         // false: shares are whole walks
+    long long size;   // chunks in a share; the first `more` have one more
     int more;
-    float *u;  // [(g - 1) fine][a][b]
-    float *e;  // [(g - 1) fine]
-    int stretches() const { return fine > 0 ? (g - 1) * fine : 0; }  // fine = 0: shares are whole walks
+    float *u;  // [g - 1][a][b]
+    float *e;  // [g - 1]
+    int stretches() const { return cut ? g - 1 : 0; }
 };
 bool tc_sizes(int dk, int dv, bool in_bf16);
 Shares tc_shares(int BH, int L, int n);

@@ -305,9 +305,9 @@ cudaError_t launch_t(const Walks &ws, Gate g, int BH, int L, const Segments &sg,
     return launch_after(full, dim3(blocks * BH, sg.n), NT, smem, s, ws, sg, g, BH, L);
 }
 
-constexpr int DL_T = 512, DL_E = 8;
+constexpr int DL_T = 512, DL_E = 8;  // tokens at once: 4096
 
-// One CTA per head, tokens from the end: a block-wide suffix sum in fp64 (the differences q.dq - k.dk
+// One CTA per head, 4096 tokens at a time from the end: a block-wide suffix sum in fp64 (the differences q.dq - k.dk
 // of a long sequence cancel down to the pairs that straddle a token).
 template <typename T>
 __global__ void __launch_bounds__(DL_T)
@@ -334,41 +334,50 @@ __global__ void __launch_bounds__(DL_T)
         __syncthreads();
     }
     const size_t row = (size_t)bh * L, plane = (size_t)BH * L;
-    for (int hi = L; hi > 0; hi -= DL_T * DL_E) {
-        // thread tid holds tokens hi - 1 - (tid DL_E + e), e = 0 .. DL_E - 1
-        double x[DL_E], sum = 0.0;
+    for (int lo = (L - 1) / (DL_T * DL_E) * (DL_T * DL_E); lo >= 0; lo -= DL_T * DL_E) {
+        // thread tid holds tokens t0 .. t0 + DL_E - 1, and the sums behind them
+        const int t0 = lo + tid * DL_E;
+        double x[DL_E];
 #pragma unroll
-        for (int e = 0; e < DL_E; ++e) {
-            const int t = hi - 1 - (tid * DL_E + e);
-            double v = 0.0;
-            if (t >= 0) {
-                for (int i = 0; i < nq; ++i) v += (double)dotq[i * plane + row + t];
-                for (int i = 0; i < nk; ++i) v -= (double)dotk[i * plane + row + t];
+        for (int e = 0; e < DL_E; ++e) x[e] = 0.0;
+        if (t0 < L) {
+            const bool whole = t0 + DL_E <= L && L % 4 == 0;  // then every row of the planes is 16-byte aligned
+            for (int i = 0; i < nq + nk; ++i) {
+                const float *p = (i < nq ? dotq + i * plane : dotk + (i - nq) * plane) + row + t0;
+                float v[DL_E];
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < DL_E; e += 4) *reinterpret_cast<float4 *>(v + e) = *reinterpret_cast<const float4 *>(p + e);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < DL_E; ++e) v[e] = t0 + e < L ? p[e] : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < DL_E; ++e) x[e] += i < nq ? (double)v[e] : -(double)v[e];
             }
-            sum += v;
-            x[e] = sum;
         }
-        double s = sum;
+#pragma unroll
+        for (int e = DL_E - 2; e >= 0; --e) x[e] += x[e + 1];
+        double s = x[0];  // inclusive over the threads behind
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
+            const double y = __shfl_down_sync(0xffffffffu, s, o);
+            if (lane + o < 32) s += y;
         }
-        if (lane == 31) part[warp] = s;
+        if (lane == 0) part[warp] = s;
         __syncthreads();
-        double before = carry;
-        for (int i = 0; i < warp; ++i) before += part[i];
-        const double off = before + (s - sum);
+        double behind = carry + (s - x[0]);
+        for (int i = DL_T / 32 - 1; i > warp; --i) behind += part[i];
 #pragma unroll
         for (int e = 0; e < DL_E; ++e) {
-            const int t = hi - 1 - (tid * DL_E + e);
-            if (t >= 0) {
+            const int t = t0 + e;
+            if (t < L) {
                 // a token that forgets everything: d e^l / dl = 0
                 const bool forgets = gate_at(g, bh, L, t) == L_MIN;
-                dlog[row + t] = from_f32<T>(forgets ? 0.f : (float)(off + x[e]));
+                dlog[row + t] = from_f32<T>(forgets ? 0.f : (float)(behind + x[e]));
             }
         }
-        if (tid == DL_T - 1) carry_s = off + sum;
+        if (tid == 0) carry_s = behind + x[0];
         __syncthreads();
         carry = carry_s;
     }

@@ -51,7 +51,6 @@ namespace {
 constexpr int WARPS = 24, THREADS = WARPS * 32;
 constexpr int W_STATE = 20, W_INTRA = 21, W_TMA = 22, W_GATE = 23;
 constexpr int NS = 3;     // stages of X, Y, Z
-constexpr int AHEAD = 4;  // chunks that are brought to L2 ahead of their load
 constexpr int GB = 4, SLOTS = 2 * GB;  // chunks whose decay weights are made at once, and kept
 constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
 
@@ -236,7 +235,7 @@ __device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
 __device__ __forceinline__ void weigh(uint32_t y, uint32_t fh, uint32_t fl, uint32_t &hi, uint32_t &lo) {
     uint32_t rest;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(fh));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(rest) : "r"(y), "r"(fh), "r"(hi ^ 0x80008000u));
+    asm("{\n\t.reg .b32 t;\n\tneg.bf16x2 t, %3;\n\tfma.rn.bf16x2 %0, %1, %2, t;\n\t}" : "=r"(rest) : "r"(y), "r"(fh), "r"(hi));
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(y), "r"(fl), "r"(rest));
 }
 
@@ -284,7 +283,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // the same direction lie alike, so that the later of two readers finds its tiles in L2.
     // This CTA's chunks, [p0, p1) of the row of all walks' chunks, or a part of such a share's last stretch
     const int NC = (L + C - 1) / C;
-    const int share = OUT ? blockIdx.x : blockIdx.x / sh.fine;
+    const int share = blockIdx.x;
     auto bound = [&](int c) { return c * sh.size + min(c, sh.more); };
     long long p0 = bound(share), p1 = bound(share + 1);
     // A place in it: the walk and its head, and the chunk's position in walking order.
@@ -304,15 +303,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     Place at;
     {
         // whole walks: a share is one; shares of cut ones are counted in 32 bits (tc_shares)
-        const uint32_t u = sh.fine == 0 ? share : (uint32_t)(OUT ? p0 : p1 - 1) / (uint32_t)NC;
+        const uint32_t u = sh.cut ? (uint32_t)(OUT ? p0 : p1 - 1) / (uint32_t)NC : share;
         at.k = (int)(p0 - (long long)u * NC);
         if (!OUT) {
             const bool ends = p1 == (long long)(u + 1) * NC;  // the share ends with a walk's end: nothing to do
             if (at.k < 0) at.k = 0;
-            const int len = ends ? 0 : (int)(p1 - (long long)u * NC) - at.k, part = (len + sh.fine - 1) / sh.fine;
-            at.k += part * (blockIdx.x % sh.fine);
-            p0 = (long long)u * NC + at.k;
-            p1 = len > 0 ? min(p1, p0 + part) : p0;
+            p0 = ends ? p1 : (long long)u * NC + at.k;
         }
         at.wi = u / BH;
         at.bh = u - at.wi * BH;
@@ -396,7 +392,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             int c0 = share;       // the first share whose last stretch is of this walk
             if (at.k > 0)
                 while (bound(c0) > p0 - at.k) --c0;
-            load_state(at, c0 * sh.fine, share * sh.fine, 16 * (wg - 2), 48);
+            load_state(at, c0, share, 16 * (wg - 2), 48);
             tc::tc_fence_before();
             tc::named_bar_sync(1, 384);
             tc::tc_fence_after();
@@ -404,25 +400,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (warp == W_TMA) {
         const bool leader = elect();
-        // Tiles come to L2 AHEAD chunks before they are loaded: shared memory holds three chunks, which covers an
-        // L2 read but not one from HBM.
-        Place far = at;
-        int n = 0, m = 0;
+        int n = 0;
         for (; n < cnt; ++n) {
-#pragma unroll 1
-            for (; m < cnt && m < n + AHEAD; ++m) {
-                const int c0 = far.chunk(NC) * C;
-                if (leader && m >= NS) {
-                    tc::tma_prefetch_4d(&maps.y[far.wi], 0, c0, 0, far.bh);
-                    if (OUT) tc::tma_prefetch_4d(&maps.x[far.wi], 0, c0, 0, far.bh);
-                    tc::tma_prefetch_4d(&maps.z[far.wi], 0, c0, 0, far.bh);
-                    if (OUT && BWD && ws.w[far.wi].dot) {
-                        tc::tma_prefetch_4d(&maps.d[far.wi], 0, c0, 0, far.bh);
-                        tc::tma_prefetch_4d(&maps.d[far.wi], 0, c0 + C / 2, 0, far.bh);
-                    }
-                }
-                next(far);
-            }
             const int st = n % NS, c0 = at.chunk(NC) * C, wi = at.wi, bh = at.bh;
             if (n >= NS && !wait(&bars.free_s[st], n / NS - 1)) break;
             uint8_t *s = base + st * K::STAGE;
@@ -455,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const bool split = BWD && ws.w[at.wi].dot;
                 if (elect()) {
                     const uint32_t o1 = tmem + K::T_O1 + ob * 64;
-#pragma unroll 2
+#pragma unroll
                     for (int kk = 0; kk < A / 16; ++kk) {
                         const uint64_t x = dx + o + ((kk >> 2) * 512 + (kk & 3) * 2);
                         tc::mma_tmem_a(o1, tmem + K::T_H + kk * 8, x, id_o1, kk > 0);
@@ -469,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tc_fence_after();
             if (elect()) {  // S^T += Z^T Yw
                 const uint64_t yh = dh + (uint64_t)((n & 1) * (K::XB >> 4));
-#pragma unroll 1
+#pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
                     tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yh + kk * 128, id_s, OUT || n > 0 || kk > 0);
                     tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, dl + kk * 128, id_s, 1u);
@@ -497,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto issue_p = [&](int n, int st) {  // P = X Y^T
             if (elect()) {
                 const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-#pragma unroll 2
+#pragma unroll
                 for (int kk = 0; kk < A / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * 512 + (kk & 3) * 2;
                     tc::mma_bf16(tmem + K::T_P + (n & 1) * 64, dx + o + off, dy + o + off, id_p, kk > 0);
@@ -523,7 +502,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tc::tc_fence_after();
             if (elect()) {  // O2^T = Z^T (D o P)^T
                 const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));
-#pragma unroll 2
+#pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
                     tc::mma_bf16(tmem + K::T_O2, z + kk * 128, dp + kk * 2, id_o2, kk > 0);
                 tc::mma_commit(&bars.o2done);
@@ -830,8 +809,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
             if (j >= 0) {
                 TO *out = static_cast<TO *>(w.out) + row0 * B + j;
+                if (!BWD && cl == 32) {  // (backwards the code that a second form takes costs more than its predicates)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], true, true);
+                } else {
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) put2(out + i * B, out + (i + 1) * B, v[i], v[i + 1], i < cl, i + 1 < cl);
+                }
             }
             if (split) {
                 if (!wait(&bars.dfull[half], loads - 1)) break;
@@ -897,8 +881,8 @@ bool tc_sizes(int dk, int dv, bool bf16) { return bf16 && (dk == 64 || dk == 128
 
 Shares tc_shares(int BH, int L, int n) {
     // In chunks of a walk: whole walks take as many rounds as the device needs for them; even shares take their
-    // length and the first pass, whose chunks cost 0.4 of a walk's and whose stretches are at most a share or a
-    // walk, in halves (two CTAs an SM follow one another), and some 6 for its launch and the states between.
+    // length, the first pass's, whose chunks cost 0.4 of a walk's and whose stretches are at most a share or most
+    // of a walk, and some 6 for its launch and the states between.
     constexpr int SMS = 148;
     const long long units = (long long)BH * n, NC = (L + C - 1) / C, total = units * NC;
     Shares sh{};
@@ -911,7 +895,7 @@ Shares tc_shares(int BH, int L, int n) {
     sh.g = (int)g;
     sh.size = total / g;
     sh.more = (int)(total % g);
-    sh.fine = even < NC ? 1 : 2;
+    sh.cut = true;
     return sh;
 }
 

@@ -130,7 +130,6 @@ __global__ void __launch_bounds__(1024) sum_dw_kernel(const float *__restrict__ 
 // one turn are neighbours (group g of a warp or block takes g, g + groups, ...), turns are a grid apart.
 template <int VEC, int NV, int G>
 struct Group {
-    static constexpr int RPC = NT / G;  // rows of a block at once
     int gl;
     __device__ __forceinline__ Group() : gl(threadIdx.x % G) {}
     __device__ __forceinline__ int at(int j) const { return (j * G + gl) * VEC; }
