@@ -18,10 +18,9 @@ __device__ __forceinline__ float gate_or_zero(const Gate &g, int bh, int L, int 
     return t < L ? gate_at(g, bh, L, t) : 0.f;
 }
 
-// A log-decay in units of log 2 / 2^32, as an integer: sums are exact (64 tokens of -200 take 47 bits), and a
-// difference of two sums keeps all of its bits where the sums themselves are in the thousands (tokens that
-// forget everything before tokens that forget little).  A scan of them takes 250 cycles a chunk; of fp64, whose
-// adds are a long dependent chain, 2900, and of pairs of fp32 600.
+// A log-decay in units of log 2 / 2^32, as an integer, for the fp32 walks: sums are exact (64 tokens of -200
+// take 47 bits), and a difference of two sums keeps all of its bits where the sums themselves are in the
+// thousands (tokens that forget everything before tokens that forget little).
 using Fixed = long long;
 constexpr float FIXED_ONE = 4294967296.f;
 constexpr Fixed FIXED_MIN = -(1LL << 60);  // a sum over many chunks stops here: 2^-(2^28) is 0

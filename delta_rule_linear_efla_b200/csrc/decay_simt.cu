@@ -217,19 +217,19 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = r4 + i;
-                float dd = 0.f;
+                double dd = 0.0;  // q.dq and k.dk cancel in dl's sums: their own rounding is kept out of them
                 if (r < cl) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         if (cc + j < nb) {
                             out[(size_t)r * b + cc + j] = from_f32<TO>(o[i][j]);
-                            if (dx) dd = fmaf(to_f32(dx[(size_t)r * b + cc + j]), o[i][j], dd);
+                            if (dx) dd += (double)to_f32(dx[(size_t)r * b + cc + j]) * (double)o[i][j];
                         }
                 }
                 if (dx) {  // the row's 16 threads are half a warp
 #pragma unroll
                     for (int off = 8; off > 0; off >>= 1) dd += __shfl_xor_sync(0xffffffffu, dd, off);
-                    if (tc == 0 && r < cl) w.dot[((size_t)blk * BH + bh) * L + t0 + r] = dd;
+                    if (tc == 0 && r < cl) w.dot[((size_t)blk * BH + bh) * L + t0 + r] = (float)dd;
                 }
             }
             __syncthreads();  // the state is read

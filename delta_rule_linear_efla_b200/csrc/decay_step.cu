@@ -88,7 +88,11 @@ __global__ void __launch_bounds__(NT)
 template <typename T, typename TO>
 void launch_t(const void *q, const void *k, const void *v, Gate g, float *S, void *o, int BH, int dk, int dv,
               cudaStream_t s) {
-    if (dv % 4 == 0)  // S is 16-byte aligned: every row is
+    // 64 columns a CTA: 24.7 us for 1024 heads of 128 x 128 (5.5 TB/s), against 26.7 with 32 and 26.8 with 128
+    if (dv % 4 == 0 && dv > 32)  // S is 16-byte aligned: every row is
+        step_kernel<T, TO, 4, 64><<<dim3(BH, (dv + 63) / 64), NT, 0, s>>>((const T *)q, (const T *)k, (const T *)v, g,
+                                                                          S, (TO *)o, BH, dk, dv);
+    else if (dv % 4 == 0)
         step_kernel<T, TO, 4, 32><<<dim3(BH, (dv + 31) / 32), NT, 0, s>>>((const T *)q, (const T *)k, (const T *)v, g,
                                                                           S, (TO *)o, BH, dk, dv);
     else

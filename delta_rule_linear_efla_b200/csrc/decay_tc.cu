@@ -11,9 +11,10 @@
 //   S^T      = e^{c_C} S^T + Z^T Yw         [b x a]      Yw = diag(w) Y
 //
 // What is rounded to bf16 on the way, and how often:
-//   D o P   once: 2^-9 of terms that add like the bf16 output itself.
-//   Yw      as two bf16 halves (Yw = hi + lo to 2^-17), two products into the fp32 state: the state is an
-//           fp32 result, and a sequence's rounding errors would gather in it.
+//   D o P   once: at most 2^-8 of terms that add like the bf16 output itself, whose own rounding is the same.
+//   Yw      as two bf16 halves (Yw = hi + lo to 2^-16), two products into the fp32 state: the state is an
+//           fp32 result, and a sequence's rounding errors would gather in it.  What is left (3e-6 of S_final at
+//           4096 tokens) is mostly the tensor core's fp32 accumulation, which truncates.
 //   S^T     once for o and for dv.  For dq and dk, whose dots with q and k give dl, as two halves: dl is
 //           a suffix sum of q.dq - k.dk that cancels down to the pairs that straddle a token; errors of
 //           D o P cancel with them (dq and dk round the same products), errors of two different state
@@ -21,6 +22,12 @@
 // Decay factors and the sums of their logarithms are fp32.  The factors within a chunk take differences of
 // running sums, off by at most 2^-10 where a chunk forgets everything at every token (sums of 18000) and 2^-15
 // with one such token: below the rounding of D o P.
+//
+// What bounds it (4 x 16 x 4096 tokens, d = 128: forward 93 us with its first pass, of which loads, stores and
+// hand-offs alone take 62 + 10; the three backward walks 310 us with theirs, of which 163): issue slots.  A
+// chunk takes about 1600 instructions a scheduler forwards and 2000 backwards, at half an instruction a
+// cycle; the tensor pipe is busy a quarter of the time.  At 1 x 16 x 65536 the forward's two passes move
+// 1.6 GB in 343 us.
 //
 // Warp roles (one CTA an SM, 24 warps):
 //   0-3   weight:  Yw's halves from Y's tile
@@ -107,9 +114,9 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
     if (lane == 0) tc::mbar_arrive(bar);
 }
 
-// Bounded wait that also gives up once another role has.  The try_wait carries a suspend-time hint (as a
-// kernel of 19 warps that mostly wait must): without one the waiting warps' polls took four of five issue
-// slots from the working ones (a chunk took 8800 cycles).
+// Bounded waits that also give up once another role has.  try_wait suspends the warp for a while: with
+// test_wait, which does not, the polls of two dozen warps that mostly wait took issue slots from the working
+// ones (105 us for a prefill of 90).
 __device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -224,13 +231,13 @@ __device__ __forceinline__ uint32_t pack(F2 a) {
     return tc::pack_bf16(v.x, v.y);
 }
 
-// Two floats as packed bf16 halves: x = hi + lo to 2^-17 of |x|.
+// Two floats as packed bf16 halves: x = hi + lo to 2^-16 of |x|.
 __device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
     hi = pack(x);
     lo = pack(fma2(f2(bf_lo(hi), bf_hi(hi)), f2(-1.f, -1.f), x));
 }
 
-// Two bf16 times a weight given as two bf16, fh + fl: hi + lo to 2^-17.  hi rounds y fh; what that leaves of the
+// Two bf16 times a weight given as two bf16, fh + fl: hi + lo to 2^-16.  hi rounds y fh; what that leaves of the
 // 16-bit product is exact in bf16, and lo adds y fl to it.
 __device__ __forceinline__ void weigh(uint32_t y, uint32_t fh, uint32_t fl, uint32_t &hi, uint32_t &lo) {
     uint32_t rest;

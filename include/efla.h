@@ -370,7 +370,15 @@ efla_status efla_bwd_kept(const void *q, const void *k, const void *v, const voi
  *   EFLA_DECAY_HEAD  -- [H] fp32, one for each head at every token
  * l is expected to be <= 0 (not checked).  -inf forgets the state, so that a row can hold
  * several documents: the first token of each carries l = -inf.  Values below -200 act as
- * -inf (e^-200 is 0 in fp32); NaN propagates.
+ * -inf (e^-200 is 0 in fp32) and values above 200 as 200; NaN reaches every later token.
+ * q, k and v are expected to be finite: within a chunk, products that the causal mask drops
+ * are taken times zero, so that an infinity or NaN of a token also reaches the earlier
+ * tokens of its chunk of 64.
+ *
+ * Two paths with the same results up to rounding: bf16 inputs with dk and dv of 64 or 128
+ * and 16-byte aligned q, k, v (and dO) run on the tensor cores with bf16 operands and fp32
+ * accumulation and state (no fp16: the range is bf16's), everything else on CUDA cores in
+ * fp32.  Results do not depend on scheduling.
  */
 typedef enum {
     EFLA_DECAY_TOKEN = 0,

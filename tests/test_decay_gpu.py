@@ -312,6 +312,33 @@ def test_offsets_past_32_bits():
     near(S[:, -1:], rS, STATE[BF])
 
 
+@pytest.mark.parametrize("size", [(3, 25, 900, 64, 128), (3, 25, 900, 128, 64), (4, 16, 1000, 128, 128), (1, 149, 700, 64, 128)])
+def test_repeats_give_the_same_bits_without_a_wait_that_gave_up(size):
+    """Cut sequences, several walks to a CTA: forty repeats of forward and backward, bit for bit."""
+    x = make(*size, BF, seed=17)
+    dO = torch.randn(x[2].shape, device="cuda").to(BF)
+
+    def run():
+        return [t for t in (*decay.decay_chunk_fwd(*x), *decay.decay_bwd(*x[:4], dO)) if t is not None]
+
+    ref = run()
+    for _ in range(40):
+        for a, b in zip(run(), ref):
+            assert torch.equal(a, b)
+    assert efla.last_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (BF, 128), (F32, 32)])
+def test_a_log_decay_that_is_not_a_number_reaches_later_tokens_only(dtype, d):
+    x = make(1, 2, 1500, d, d, dtype, s0=True, seed=18)
+    ref, _ = decay.decay_chunk_fwd(*x)
+    at = 700
+    x[3][0, 1, at] = float("nan")
+    o, S = decay.decay_chunk_fwd(*x)
+    assert torch.equal(o[0, 0], ref[0, 0]) and torch.equal(o[0, 1, :at], ref[0, 1, :at])
+    assert torch.isnan(o[0, 1, at:]).all() and torch.isnan(S[0, 1]).all() and torch.isfinite(S[0, 0]).all()
+
+
 def test_rows_behind_the_output_are_left_alone():
     x = make(1, 1, 70, 128, 128, BF, seed=16)
     buf = torch.full((2 * 70 * 128,), 7.0, dtype=BF, device="cuda")

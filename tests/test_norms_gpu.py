@@ -134,6 +134,27 @@ def test_residual_in_place_and_repeatable():
     assert y is r and torch.equal(y, ref)
 
 
+def test_broadcast_gate_and_residual():
+    """Views whose tokens or heads are one and the same (strides of zero)."""
+    o = rnd(2, 4, 50, 128, dtype=BF, seed=1)
+    gate = rnd(2, 50, 1, 128, dtype=BF, seed=2).expand(2, 50, 4, 128)
+    res = rnd(1, 1, 4, 128, dtype=BF, seed=3).expand(2, 50, 4, 128)
+    near(norms.gated_norm_fwd(o, gate, None, res), R.gated_norm(o, gate, None, res, 1.0, 1e-6, "silu"), BF)
+    dy = rnd(2, 50, 4, 128, dtype=BF, seed=4)
+    a, b = norms.gated_norm_bwd(o, gate, dy), norms.gated_norm_bwd(o, gate.contiguous(), dy)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_another_stream():
+    o, gate = rnd(1, 4, 500, 128, dtype=BF, seed=1), rnd(1, 500, 4, 128, dtype=BF, seed=2)
+    ref = norms.gated_norm_fwd(o, gate)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    y = norms.gated_norm_fwd(o, gate, stream=s)
+    s.synchronize()
+    assert torch.equal(y, ref)
+
+
 def test_autograd_and_capture():
     x, w = rnd(1, 40, 2, 64, dtype=BF, seed=1).requires_grad_(True), rnd(64, dtype=F32, seed=2).requires_grad_(True)
     dy = rnd(1, 2, 40, 64, dtype=BF, seed=3)
