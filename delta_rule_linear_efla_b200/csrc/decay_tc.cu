@@ -13,8 +13,9 @@
 // What is rounded to bf16 on the way, and how often:
 //   D o P   once: at most 2^-8 of terms that add like the bf16 output itself, whose own rounding is the same.
 //   Yw      as two bf16 halves (Yw = hi + lo to 2^-16), two products into the fp32 state: the state is an
-//           fp32 result, and a sequence's rounding errors would gather in it.  What is left (3e-6 of S_final at
-//           4096 tokens) is mostly the tensor core's fp32 accumulation, which truncates.
+//           fp32 result, and a sequence's rounding errors would gather in it.  What is left is that (2.5e-6 of
+//           S_final) and the tensor core's fp32 accumulation, which truncates: 3e-8 of the state a product, eight a
+//           chunk, 5e-6 for heads that remember 2000 tokens.
 //   S^T     once for o and for dv.  For dq and dk, whose dots with q and k give dl, as two halves: dl is
 //           a suffix sum of q.dq - k.dk that cancels down to the pairs that straddle a token; errors of
 //           D o P cancel with them (dq and dk round the same products), errors of two different state
@@ -58,6 +59,7 @@ namespace {
 constexpr int WARPS = 24, THREADS = WARPS * 32;
 constexpr int W_STATE = 20, W_INTRA = 21, W_TMA = 22, W_GATE = 23;
 constexpr int NS = 3;     // stages of X, Y, Z
+constexpr int FL = 4;     // chunks that the first pass adds up on the tensor cores
 constexpr int GB = 4, SLOTS = 2 * GB;  // chunks whose decay weights are made at once, and kept
 constexpr long long WAIT_BUDGET = 2000000000LL;  // ~1 s of SM cycles
 
@@ -86,7 +88,7 @@ struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
     uint64_t full[NS], gready[2], y_free[2], pdone[2], d2done, o1done[2], o2done, o2read, drain[2], dfull[2], l_free;
     // one arrival from each of four warps
-    uint64_t p_ready, s_ready;
+    uint64_t p_ready, s_ready;  // without output: an accumulator of the sum's parts is free again (pdone: it is full)
     uint64_t gfree[2], o_free[2];  // the eight output warps (without output, gfree: the weights' sixteen)
     uint64_t y_ready[2];               // the weights' four warps, sixteen without output
     uint64_t free_s[NS];               // one from each issuer
@@ -96,7 +98,7 @@ constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 1 + 2 + 2 + 2
 
 struct Slot {
     float qw[C];
-    uint32_t kw[C];  // a key's weight as two bf16: hi (low half) + lo
+    float kw[C];
     float gw[C];  // 2^(c_end - c) within a token's group of eight (end: its last token in walking order)
     float c2[C];  // running sum in units of log 2 (its negative backwards)
     float tot, pad[3];
@@ -235,15 +237,6 @@ __device__ __forceinline__ uint32_t pack(F2 a) {
 __device__ __forceinline__ void split2(F2 x, uint32_t &hi, uint32_t &lo) {
     hi = pack(x);
     lo = pack(fma2(f2(bf_lo(hi), bf_hi(hi)), f2(-1.f, -1.f), x));
-}
-
-// Two bf16 times a weight given as two bf16, fh + fl: hi + lo to 2^-16.  hi rounds y fh; what that leaves of the
-// 16-bit product is exact in bf16, and lo adds y fl to it.
-__device__ __forceinline__ void weigh(uint32_t y, uint32_t fh, uint32_t fl, uint32_t &hi, uint32_t &lo) {
-    uint32_t rest;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(fh));
-    asm("{\n\t.reg .b32 t;\n\tneg.bf16x2 t, %3;\n\tfma.rn.bf16x2 %0, %1, %2, t;\n\t}" : "=r"(rest) : "r"(y), "r"(fh), "r"(hi));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(lo) : "r"(y), "r"(fl), "r"(rest));
 }
 
 // The sums over a warp's lanes of 32 columns: lane l ends with column l's.
@@ -452,17 +445,21 @@ __global__ void __launch_bounds__(THREADS, 1)
                 __syncwarp();
             }
             if (!wait_all(&bars.y_ready[n & 1], n >> 1)) break;
+            const int part = n / FL;  // first pass: of the sum, in one of two accumulators
+            if (!OUT && n % FL == 0 && part >= 2 && !wait_all(part & 1 ? &bars.s_ready : &bars.p_ready, part / 2 - 1)) break;
+            const uint32_t acc = tmem + K::T_S + (OUT ? 0 : (part & 1) * A);
             tc::tc_fence_after();
             if (elect()) {  // S^T += Z^T Yw
                 const uint64_t yh = dh + (uint64_t)((n & 1) * (K::XB >> 4));
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, yh + kk * 128, id_s, OUT || n > 0 || kk > 0);
-                    tc::mma_bf16(tmem + K::T_S, dz + o + kk * 128, dl + kk * 128, id_s, 1u);
+                    tc::mma_bf16(acc, dz + o + kk * 128, yh + kk * 128, id_s, OUT || n % FL > 0 || kk > 0);
+                    tc::mma_bf16(acc, dz + o + kk * 128, dl + kk * 128, id_s, 1u);
                 }
                 tc::mma_commit(&bars.d2done);
                 tc::mma_commit(&bars.y_free[n & 1]);
                 tc::mma_commit(&bars.l_free);
+                if (!OUT && (n % FL == FL - 1 || n == cnt - 1)) tc::mma_commit(&bars.pdone[part & 1]);
             }
             if (elect()) tc::mma_commit(&bars.free_s[st]);
             __syncwarp();
@@ -590,17 +587,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             Slot &sl = slots[bi * GB + gk];
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
-                float q[4];
-                uint32_t k[4];
+                float q[4], k[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float up = ex2(before + c[i + e]), down = ex2(behind + d[i + e]);
-                    const float w = after * (rev ? up : down);
+                    k[e] = after * (rev ? up : down);
                     q[e] = rev ? down : up;
-                    const float hi = __bfloat162float(__float2bfloat16_rn(w));
-                    k[e] = tc::pack_bf16(hi, w - hi);
                 }
-                *reinterpret_cast<uint4 *>(sl.kw + tk + i) = make_uint4(k[0], k[1], k[2], k[3]);
+                *reinterpret_cast<float4 *>(sl.kw + tk + i) = make_float4(k[0], k[1], k[2], k[3]);
                 if (OUT) *reinterpret_cast<float4 *>(sl.qw + tk + i) = make_float4(q[0], q[1], q[2], q[3]);
             }
             if (OUT) {
@@ -629,18 +623,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             const uint4 *y = reinterpret_cast<const uint4 *>(base + (n % NS) * K::STAGE + K::OFF_Y) + i0;
             uint4 *hi = reinterpret_cast<uint4 *>(base + K::OFF_W + (n & 1) * K::XB) + i0;
             uint4 *lo = reinterpret_cast<uint4 *>(base + K::OFF_L) + i0;
-            const uint32_t *kw = slots[n % SLOTS].kw;
+            const float *kw = slots[n % SLOTS].kw;
             uint4 l[PIECES];
 #pragma unroll
             for (int i = 0; i < PIECES; ++i) {  // 8 pieces of 16 bytes a row of a 64-column slab
-                const uint32_t f = kw[(i0 + i * T) >> 3 & 63];
-                const uint32_t fh = __byte_perm(f, f, 0x1010), fl = __byte_perm(f, f, 0x3232);
+                const float w1 = kw[(i0 + i * T) >> 3 & 63];
+                const F2 f = f2(w1, w1);
                 const uint4 u = y[i * T];
                 uint4 h;
-                weigh(u.x, fh, fl, h.x, l[i].x);
-                weigh(u.y, fh, fl, h.y, l[i].y);
-                weigh(u.z, fh, fl, h.z, l[i].z);
-                weigh(u.w, fh, fl, h.w, l[i].w);
+                split2(f * f2(bf_lo(u.x), bf_hi(u.x)), h.x, l[i].x);
+                split2(f * f2(bf_lo(u.y), bf_hi(u.y)), h.y, l[i].y);
+                split2(f * f2(bf_lo(u.z), bf_hi(u.z)), h.z, l[i].z);
+                split2(f * f2(bf_lo(u.w), bf_hi(u.w)), h.w, l[i].w);
                 hi[i * T] = h;
             }
             if (n >= 1 && !wait(&bars.l_free, n - 1)) break;
@@ -650,18 +644,33 @@ __global__ void __launch_bounds__(THREADS, 1)
             warp_arrive(&bars.y_ready[n & 1], lane);
             if (!OUT && lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
         }
-        if (!OUT && wg == 0 && wait(&bars.drain[0], 0)) {  // the segment's contribution
-            const int j = acc_row<B>(warp, lane);
-            float *sout = sh.u + (size_t)blockIdx.x * A * B;
+    } else if (!OUT && wg == 4) {
+        // The stretch's contribution.  The tensor core truncates its fp32 sums, and a stretch is up to a hundred
+        // chunks of eight products, whose older ones add little or nothing to a large sum: off by 2e-4 in all.  So
+        // it adds up four chunks at a time, and these are added here, rounded to nearest.
+        const int j = acc_row<B>(warp & 3, lane), parts = (cnt + FL - 1) / FL;
+        float *u = sh.u + (size_t)blockIdx.x * A * B;
+        for (int f = 0; f < parts; ++f) {
+            if (!wait(&bars.pdone[f & 1], f >> 1)) break;
             tc::tc_fence_after();
 #pragma unroll 1
             for (int cb = 0; cb < A; cb += 16) {
                 float v[16];
-                tc::tmem_ld16(tmem + lane_base + K::T_S + cb, v);
-                if (j >= 0)
+                tc::tmem_ld16(tmem + lane_base + K::T_S + (f & 1) * A + cb, v);
+                if (f > 0) {
+                    float s[16];
+                    tc::tmem_ld16(tmem + lane_base + K::T_S + 2 * A + cb, s);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sout[(size_t)(cb + i) * B + j] = cnt > 0 ? v[i] : 0.f;
+                    for (int i = 0; i < 16; ++i) v[i] += s[i];
+                }
+                if (f < parts - 1) {
+                    tc::tmem_st16(tmem + lane_base + K::T_S + 2 * A + cb, v);
+                } else if (j >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) u[(size_t)(cb + i) * B + j] = v[i];
+                }
             }
+            warp_arrive(f & 1 ? &bars.s_ready : &bars.p_ready, lane);
         }
     } else if (OUT && wg == 1) {
         // ---------------------------------------------------------- D o P

@@ -378,7 +378,9 @@ efla_status efla_bwd_kept(const void *q, const void *k, const void *v, const voi
  * Two paths with the same results up to rounding: bf16 inputs with dk and dv of 64 or 128
  * and 16-byte aligned q, k, v (and dO) run on the tensor cores with bf16 operands and fp32
  * accumulation and state (no fp16: the range is bf16's), everything else on CUDA cores in
- * fp32.  Results do not depend on scheduling.
+ * fp32.  Results do not depend on scheduling.  The tensor-core path's states (S_final, dS0)
+ * are off by about 3e-6 in the 2-norm, and by 2.4e-7 more for every chunk of 64 tokens that
+ * the state remembers (its accumulation truncates).
  */
 typedef enum {
     EFLA_DECAY_TOKEN = 0,
