@@ -38,43 +38,116 @@ struct Lay {
     }
 };
 
-// rows [t0, t0 + C) of a [L][d] tensor, columns [j0, j0 + n), zero past L and past d.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(float *dst, const void *src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src),
+                 "n"(BYTES), "r"(on ? BYTES : 0)
+                 : "memory");
+}
+
+// Rows 0 .. C - 1 of src [][d], columns [j0, j0 + n), zero from row cl and column d on.  fp32 comes by asynchronous
+// copies, all in flight at once; copies_done() waits for the thread's own.
 template <typename T>
-__device__ __forceinline__ void load_tile(float *dst, int pitch, const T *src, int d, int j0, int n, int cl,
-                                          int tid) {
+__device__ __forceinline__ void load_tile(float *dst, int pitch, const T *src, int d, int j0, int n, int cl, int tid) {
     constexpr int V = 16 / sizeof(T);
-    const bool vec = (reinterpret_cast<uintptr_t>(src) % 16 == 0) && d % V == 0 && n % V == 0 && j0 + n <= d;
-    if (vec) {
-        const int per = n / V;
-        for (int e = tid; e < C * per; e += NT) {
-            const int r = e / per, c = (e - r * per) * V;
-            float f[V];
-            if (r < cl) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(src + (size_t)r * d + j0 + c);
-                const T *h = reinterpret_cast<const T *>(&u);
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = to_f32(h[i]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) f[i] = 0.f;
-            }
+    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && d % V == 0 && n % V == 0;
+    const int per = vec ? n / V : n, step = NT / per, c = tid % per * (vec ? V : 1);  // per <= 128
+    int r = tid / per;
+    if (r >= step) return;
+    dst += r * pitch + c;
+    const bool in = j0 + c < d;
+    const T *p = src + (in ? (size_t)r * d + j0 + c : 0);
+    if constexpr (sizeof(T) == 4) {
+        if (vec)
+            for (; r < C; r += step, dst += step * pitch, p += step * d) copy_async<16>(dst, in && r < cl ? p : src, in && r < cl);
+        else
+            for (; r < C; r += step, dst += step * pitch, p += step * d) copy_async<4>(dst, in && r < cl ? p : src, in && r < cl);
+    } else if (vec) {
+#pragma unroll 4
+        for (; r < C; r += step, dst += step * pitch, p += step * d) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (in && r < cl) u = *reinterpret_cast<const uint4 *>(p);
+            const T *h = reinterpret_cast<const T *>(&u);
 #pragma unroll
             for (int i = 0; i < V; i += 4)
-                *reinterpret_cast<float4 *>(dst + r * pitch + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+                *reinterpret_cast<float4 *>(dst + i) = make_float4(to_f32(h[i]), to_f32(h[i + 1]), to_f32(h[i + 2]), to_f32(h[i + 3]));
         }
     } else {
-        for (int e = tid; e < C * n; e += NT) {
-            const int r = e / n, c = e - r * n;
-            dst[r * pitch + c] = (r < cl && j0 + c < d) ? to_f32(src[(size_t)r * d + j0 + c]) : 0.f;
-        }
+#pragma unroll 8
+        for (; r < C; r += step, dst += step * pitch, p += step * d) *dst = in && r < cl ? to_f32(*p) : 0.f;
     }
 }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void fma4(float (&acc)[4], float s, const float4 &v) {
     acc[0] = fmaf(s, v.x, acc[0]);
     acc[1] = fmaf(s, v.y, acc[1]);
     acc[2] = fmaf(s, v.z, acc[2]);
     acc[3] = fmaf(s, v.w, acc[3]);
+}
+
+// Rows r .. r + 3 of P = D o (X Y^T), at columns c, c + 16, .. (NJ of them).
+template <int NJ>
+__device__ __forceinline__ void scores(float *P, const float *X, const float *Y, int xp, int ap, const float *chi,
+                                       const float *clo, int r, int c, bool rev) {
+    float p[4][NJ];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) p[i][j] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < ap; k += 4) {
+        float4 xv[4], yv[NJ];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const float4 *>(X + (r + i) * xp + k);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) yv[j] = *reinterpret_cast<const float4 *>(Y + (c + 16 * j) * xp + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                p[i][j] = fmaf(xv[i].x, yv[j].x, fmaf(xv[i].y, yv[j].y, fmaf(xv[i].z, yv[j].z, fmaf(xv[i].w, yv[j].w, p[i][j]))));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int t = r + i, u = c + 16 * j;
+            const float d = (chi[t] - chi[u]) + (clo[t] - clo[u]);
+            P[t * PP + u] = (rev ? u >= t : u <= t) ? p[i][j] * exp2f(rev ? -d : d) : 0.f;
+        }
+}
+
+// S <- e S + Y^T diag(kw) Z over n tokens: RT x 4 elements a thread, so that its 256 threads cover 32 RT rows.
+template <int RT>
+__device__ __forceinline__ void update_state(float *S, const float *Y, const float *Z, const float *kw, float e, int xp,
+                                             int ap, int n, int tid) {
+    const int si = (tid >> 3) * RT, sc = (tid & 7) * 4;
+    if (si >= ap) return;
+    float acc[RT][4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int t = 0; t < n; ++t) {
+        float yv[RT];
+        if constexpr (RT == 4) *reinterpret_cast<float4 *>(yv) = *reinterpret_cast<const float4 *>(Y + t * xp + si);
+        else *reinterpret_cast<float2 *>(yv) = *reinterpret_cast<const float2 *>(Y + t * xp + si);
+        float4 zv = *reinterpret_cast<const float4 *>(Z + t * ZP + sc);
+        const float f = kw[t];
+        zv.x *= f; zv.y *= f; zv.z *= f; zv.w *= f;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) fma4(acc[i], yv[i], zv);
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        float4 *s4 = reinterpret_cast<float4 *>(S + (si + i) * ZP + sc);
+        float4 s = *s4;
+        s.x = fmaf(e, s.x, acc[i][0]); s.y = fmaf(e, s.y, acc[i][1]);
+        s.z = fmaf(e, s.z, acc[i][2]); s.w = fmaf(e, s.w, acc[i][3]);
+        *s4 = s;
+    }
 }
 
 // OUT = false: the stretch's own contribution to the state only (segments' first pass).
@@ -106,25 +179,51 @@ __global__ void __launch_bounds__(NT, 2)
     const size_t sbh = (size_t)bh * a * b;
     const float *s0 = OUT && w.s0 ? w.s0 + sbh : nullptr;
     const float *eb = sg.e + ((size_t)(rev ? 1 : 0) * BH + bh) * (sg.n - 1), *ub = sg.u[wi] + (size_t)bh * (sg.n - 1) * a * b;
-    for (int e = tid; e < ap * BT; e += NT) {
-        const int i = e / BT, j = e % BT;
-        float v = 0.f;
-        if (OUT && i < a && j < nb) {
-            if (s0) v = w.s0_t ? s0[(size_t)(j0 + j) * a + i] : s0[(size_t)i * b + j0 + j];
-            for (int k = 0; k < seg; ++k) v = fmaf(eb[k], v, ub[(size_t)k * a * b + (size_t)i * b + j0 + j]);
+    if (OUT && s0 && w.s0_t) {
+        for (int e = tid; e < a * nb; e += NT) {  // along the stored rows
+            const int j = e / a, i = e - j * a;
+            S[i * ZP + j] = s0[(size_t)(j0 + j) * a + i];
         }
-        S[i * ZP + j] = v;
+        __syncthreads();
+    }
+    {
+        constexpr int PER = 128 / (NT / BT);  // a <= 128
+        const int i0 = tid / BT, j = tid % BT;
+        float v[PER];
+#pragma unroll
+        for (int m = 0; m < PER; ++m) {
+            const int i = i0 + m * (NT / BT);
+            v[m] = OUT && s0 && i < a && j < nb ? (w.s0_t ? S[i * ZP + j] : s0[(size_t)i * b + j0 + j]) : 0.f;
+        }
+        if (OUT && j < nb)
+            for (int k = 0; k < seg; ++k) {
+                const float e = eb[k], *u = ub + (size_t)k * a * b + (size_t)i0 * b + j0 + j;
+#pragma unroll
+                for (int m = 0; m < PER; ++m)
+                    if (i0 + m * (NT / BT) < a) v[m] = fmaf(e, v[m], u[(size_t)m * (NT / BT) * b]);
+            }
+#pragma unroll
+        for (int m = 0; m < PER; ++m)
+            if (i0 + m * (NT / BT) < ap) S[(i0 + m * (NT / BT)) * ZP + j] = v[m];
     }
     Fixed seg_sum = 0;
     bool seg_good = true;
 
-    const int r4 = (tid >> 4) * 4, tc = tid & 15;  // P: rows r4.., columns tc + 16 j; out: columns 2 tc, 2 tc + 1
+    // P: rows r4.., columns tc + 16 j up to the diagonal; out: columns 2 tc, 2 tc + 1.  Warps w and w + 4, which an
+    // SM's scheduler holds together, have five column blocks of P between them.
+    const int r4 = 8 * (warp < 4 ? warp : 11 - warp) + 4 * (lane >> 4), tc = tid & 15;
+    const int jb = r4 / 16, j_lo = rev ? jb : 0, nj = rev ? 4 - jb : jb + 1;
+    const size_t head = (size_t)bh * L;
+    auto load_x = [&](int it) {
+        const int t0 = (rev ? NC - 1 - it : it) * C;
+        load_tile(X, xp, static_cast<const T *>(w.x) + (head + t0) * a, a, 0, ap, min(C, L - t0), tid);
+    };
+    if (OUT) load_x(i0);
     for (int it = i0; it < i1; ++it) {
         const int n = rev ? NC - 1 - it : it;
         const int t0 = n * C, cl = min(C, L - t0);
-        const size_t row0 = (size_t)bh * L + t0;
+        const size_t row0 = head + t0;
         __syncthreads();  // the chunk before is done with every buffer
-        if (OUT) load_tile(X, xp, static_cast<const T *>(w.x) + row0 * a, a, 0, ap, cl, tid);
         load_tile(Y, xp, static_cast<const T *>(w.y) + row0 * a, a, 0, ap, cl, tid);
         load_tile(Z, ZP, static_cast<const T *>(w.z) + row0 * b, b, j0, BT, cl, tid);
         if (warp == 0) {
@@ -145,42 +244,25 @@ __global__ void __launch_bounds__(NT, 2)
             seg_sum = max(seg_sum + c.cC, FIXED_MIN);
             seg_good = seg_good && c.bad == C;
         }
+        copies_done();
         __syncthreads();
         if (OUT) {
-            // ---- P = D o (X Y^T): 4 x 4 a thread
-            float p[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) p[i][j] = 0.f;
-            for (int k = 0; k < ap; k += 4) {
-                float4 xv[4], yv[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const float4 *>(X + (r4 + i) * xp + k);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) yv[j] = *reinterpret_cast<const float4 *>(Y + (tc + 16 * j) * xp + k);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        p[i][j] = fmaf(xv[i].x, yv[j].x, fmaf(xv[i].y, yv[j].y, fmaf(xv[i].z, yv[j].z, fmaf(xv[i].w, yv[j].w, p[i][j]))));
+            if (r4 < cl) {
+                const int c0 = tc + 16 * j_lo;
+                if (nj == 1) scores<1>(P, X, Y, xp, ap, chi, clo, r4, c0, rev);
+                else if (nj == 2) scores<2>(P, X, Y, xp, ap, chi, clo, r4, c0, rev);
+                else if (nj == 3) scores<3>(P, X, Y, xp, ap, chi, clo, r4, c0, rev);
+                else scores<4>(P, X, Y, xp, ap, chi, clo, r4, c0, rev);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = r4 + i, c = tc + 16 * j;
-                    const float d = (chi[r] - chi[c]) + (clo[r] - clo[c]);
-                    const bool on = rev ? c >= r : c <= r;
-                    P[r * PP + c] = on ? p[i][j] * exp2f(rev ? -d : d) : 0.f;
-                }
             __syncthreads();
             // ---- out = diag(q) X S + P Z: 4 rows x 2 columns a thread
             float o[4][2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i][0] = o[i][1] = 0.f;
             const int cc = 2 * tc;
-            for (int k = 0; k < ap; k += 4) {
+            const int ka = r4 < cl ? ap : 0;
+#pragma unroll 2
+            for (int k = 0; k < ka; k += 4) {
                 float4 xv[4];
                 float2 sv[4];
 #pragma unroll
@@ -198,7 +280,8 @@ __global__ void __launch_bounds__(NT, 2)
                 o[i][0] *= qw[r4 + i];
                 o[i][1] *= qw[r4 + i];
             }
-            const int k0 = rev ? r4 : 0, k1 = rev ? C : r4 + 4;  // the rest of P's rows is zero
+            const int k0 = rev ? r4 : 0, k1 = r4 >= cl ? k0 : rev ? cl : r4 + 4;  // the rest of P's rows, or of Z, is zero
+#pragma unroll 2
             for (int k = k0; k < k1; k += 4) {
                 float4 pv[4];
                 float2 zv[4];
@@ -232,37 +315,11 @@ __global__ void __launch_bounds__(NT, 2)
                     if (tc == 0 && r < cl) w.dot[((size_t)blk * BH + bh) * L + t0 + r] = (float)dd;
                 }
             }
-            __syncthreads();  // the state is read
+            __syncthreads();  // the state and X are read
+            if (it + 1 < i1) load_x(it + 1);
         }
-        // ---- S <- e^{c_C} S + Y^T diag(w) Z: 4 x 4 a thread
-        const float e = tot[0];
-        const int sc = (tid & 7) * 4;
-        for (int si = (tid >> 3) * 4; si < ap; si += (NT / 8) * 4) {
-            float acc[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 4
-            for (int t = 0; t < C; ++t) {
-                const float4 yv = *reinterpret_cast<const float4 *>(Y + t * xp + si);
-                float4 zv = *reinterpret_cast<const float4 *>(Z + t * ZP + sc);
-                const float f = kw[t];
-                zv.x *= f; zv.y *= f; zv.z *= f; zv.w *= f;
-                fma4(acc[0], yv.x, zv);
-                fma4(acc[1], yv.y, zv);
-                fma4(acc[2], yv.z, zv);
-                fma4(acc[3], yv.w, zv);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float4 *s4 = reinterpret_cast<float4 *>(S + (si + i) * ZP + sc);
-                float4 s = *s4;
-                s.x = fmaf(e, s.x, acc[i][0]); s.y = fmaf(e, s.y, acc[i][1]);
-                s.z = fmaf(e, s.z, acc[i][2]); s.w = fmaf(e, s.w, acc[i][3]);
-                *s4 = s;
-            }
-        }
+        if (ap > 64) update_state<4>(S, Y, Z, kw, tot[0], xp, ap, cl, tid);
+        else update_state<2>(S, Y, Z, kw, tot[0], xp, ap, cl, tid);
     }
     __syncthreads();
     float *sout = nullptr;
@@ -386,20 +443,25 @@ __global__ void __launch_bounds__(DL_T)
 }  // namespace
 
 Segments simt_segments(int BH, int L, const int *blocks, int n) {
-    // A segment run more costs about a third of a walk (the state update alone); below about one CTA
-    // an SM the sequence is cut until the device is full, at four chunks a segment or more.
+    // In chunks of a walk: two CTAs an SM take rounds of n segments' chunks each, a first pass (the state update
+    // alone) another 0.35 of them, joining the states of the segments before some 0.1 a segment, and the launch 1.
+    constexpr int SLOTS = 2 * 148;
     Segments sg{};
     long long ctas = 0;
     for (int i = 0; i < n; ++i) ctas += (long long)blocks[i] * BH;
     const int NC = (L + C - 1) / C;
     sg.n = 1;
     sg.chunks = NC;
-    if (ctas >= 148) return sg;
-    long long want = (2 * 148 + ctas - 1) / ctas;
-    if (want > NC / 4) want = NC / 4;
-    if (want < 2) return sg;
-    sg.chunks = (int)((NC + want - 1) / want);
-    sg.n = (NC + sg.chunks - 1) / sg.chunks;
+    double best = (double)((ctas + SLOTS - 1) / SLOTS) * NC;
+    for (int k = 2; k <= NC / 2 && ctas * k <= 4 * SLOTS; ++k) {
+        const int chunks = (NC + k - 1) / k, m = (NC + chunks - 1) / chunks;
+        const double cost = (double)((ctas * m + SLOTS - 1) / SLOTS) * chunks * 1.35 + 0.1 * m + 1.;
+        if (cost < best) {
+            best = cost;
+            sg.n = m;
+            sg.chunks = chunks;
+        }
+    }
     return sg;
 }
 
