@@ -7,11 +7,18 @@
 //   P = D o (X Y^T) (64 x 64),   out = diag(q) X S + P Z,   S <- e^{c_C} S + Y^T diag(w) Z
 //
 // with D, q and w the decay weights of decay.h.  Every product is register-tiled out of shared
-// memory (4 x 4 or 4 x 2 outputs a thread, 16-byte loads along the inner dimension), so the FMA pipe
-// and shared memory take about the same time.  32 columns keep a CTA at 113 KB, two to an SM, so
-// that one's loads run under the other's arithmetic; P is computed again in each column block.
+// memory (4 x 4 or 4 x 2 outputs a thread, 16-byte loads along the inner dimension).  32 columns keep
+// a CTA at 113 KB, two to an SM, so that one's loads run under the other's arithmetic; P is computed
+// again in each column block, up to its diagonal.
+//
+// What bounds it (fp32, 8 x 32 x 256 tokens, d = 128: 319 us): shared memory's wavefronts (68 % of their
+// rate) and issue slots (59 %); a chunk of one column block takes 53,000 warp instructions, 29,000 of them FMAs.
+// Short sequences of few heads wait for their chain of chunks: cut into segments of two or more chunks,
+// 2 x 3 x 777 tokens take 46 us (76 with four or more, whose loads and joins waited for one another).
 #include "decay_gate.cuh"
 #include "launchers.h"
+
+#include <type_traits>
 
 namespace efla {
 namespace decay {
@@ -45,36 +52,44 @@ __device__ __forceinline__ void copy_async(float *dst, const void *src, bool on)
                  : "memory");
 }
 
-// Rows 0 .. C - 1 of src [][d], columns [j0, j0 + n), zero from row cl and column d on.  fp32 comes by asynchronous
-// copies, all in flight at once; copies_done() waits for the thread's own.
-template <typename T>
-__device__ __forceinline__ void load_tile(float *dst, int pitch, const T *src, int d, int j0, int n, int cl, int tid) {
-    constexpr int V = 16 / sizeof(T);
-    const bool vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && d % V == 0 && n % V == 0;
-    const int per = vec ? n / V : n, step = NT / per, c = tid % per * (vec ? V : 1);  // per <= 128
+// V elements a thread and row, V * sizeof(T) bytes at once; d and n are multiples of V.
+template <int V, typename T>
+__device__ __forceinline__ void load_rows(float *dst, int pitch, const T *src, int d, int j0, int n, int cl, int tid) {
+    const int per = n / V, step = NT / per, c = tid % per * V;  // per <= 128
     int r = tid / per;
     if (r >= step) return;
     dst += r * pitch + c;
     const bool in = j0 + c < d;
     const T *p = src + (in ? (size_t)r * d + j0 + c : 0);
     if constexpr (sizeof(T) == 4) {
-        if (vec)
-            for (; r < C; r += step, dst += step * pitch, p += step * d) copy_async<16>(dst, in && r < cl ? p : src, in && r < cl);
-        else
-            for (; r < C; r += step, dst += step * pitch, p += step * d) copy_async<4>(dst, in && r < cl ? p : src, in && r < cl);
-    } else if (vec) {
-#pragma unroll 4
+        for (; r < C; r += step, dst += step * pitch, p += step * d)
+            copy_async<4 * V>(dst, in && r < cl ? p : src, in && r < cl);
+    } else {
+        using U = std::conditional_t<V == 8, uint4, std::conditional_t<V == 4, uint2, std::conditional_t<V == 2, unsigned, unsigned short>>>;
+#pragma unroll 8
         for (; r < C; r += step, dst += step * pitch, p += step * d) {
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (in && r < cl) u = *reinterpret_cast<const uint4 *>(p);
+            U u{};
+            if (in && r < cl) u = *reinterpret_cast<const U *>(p);
             const T *h = reinterpret_cast<const T *>(&u);
 #pragma unroll
-            for (int i = 0; i < V; i += 4)
-                *reinterpret_cast<float4 *>(dst + i) = make_float4(to_f32(h[i]), to_f32(h[i + 1]), to_f32(h[i + 2]), to_f32(h[i + 3]));
+            for (int i = 0; i < V; ++i) dst[i] = to_f32(h[i]);
         }
+    }
+}
+
+// Rows 0 .. C - 1 of src [][d], columns [j0, j0 + n), zero from row cl and column d on.  fp32 comes by asynchronous
+// copies, all in flight at once; copies_done() waits for the thread's own.
+template <typename T>
+__device__ __forceinline__ void load_tile(float *dst, int pitch, const T *src, int d, int j0, int n, int cl, int tid) {
+    const unsigned at = (unsigned)reinterpret_cast<uintptr_t>(src) / (unsigned)sizeof(T) | d | n;  // src, rows and n: multiples of V?
+    if constexpr (sizeof(T) == 4) {
+        if (at % 4 == 0) load_rows<4>(dst, pitch, src, d, j0, n, cl, tid);
+        else load_rows<1>(dst, pitch, src, d, j0, n, cl, tid);
     } else {
-#pragma unroll 8
-        for (; r < C; r += step, dst += step * pitch, p += step * d) *dst = in && r < cl ? to_f32(*p) : 0.f;
+        if (at % 8 == 0) load_rows<8>(dst, pitch, src, d, j0, n, cl, tid);
+        else if (at % 4 == 0) load_rows<4>(dst, pitch, src, d, j0, n, cl, tid);
+        else if (at % 2 == 0) load_rows<2>(dst, pitch, src, d, j0, n, cl, tid);
+        else load_rows<1>(dst, pitch, src, d, j0, n, cl, tid);
     }
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -196,6 +211,7 @@ __global__ void __launch_bounds__(NT, 2)
             v[m] = OUT && s0 && i < a && j < nb ? (w.s0_t ? S[i * ZP + j] : s0[(size_t)i * b + j0 + j]) : 0.f;
         }
         if (OUT && j < nb)
+#pragma unroll 2
             for (int k = 0; k < seg; ++k) {
                 const float e = eb[k], *u = ub + (size_t)k * a * b + (size_t)i0 * b + j0 + j;
 #pragma unroll
@@ -444,7 +460,7 @@ __global__ void __launch_bounds__(DL_T)
 
 Segments simt_segments(int BH, int L, const int *blocks, int n) {
     // In chunks of a walk: two CTAs an SM take rounds of n segments' chunks each, a first pass (the state update
-    // alone) another 0.35 of them, joining the states of the segments before some 0.1 a segment, and the launch 1.
+    // alone) another 0.35 of them, joining the states of the segments before some 0.05 a segment, and the launch 1.
     constexpr int SLOTS = 2 * 148;
     Segments sg{};
     long long ctas = 0;
@@ -455,7 +471,7 @@ Segments simt_segments(int BH, int L, const int *blocks, int n) {
     double best = (double)((ctas + SLOTS - 1) / SLOTS) * NC;
     for (int k = 2; k <= NC / 2 && ctas * k <= 4 * SLOTS; ++k) {
         const int chunks = (NC + k - 1) / k, m = (NC + chunks - 1) / chunks;
-        const double cost = (double)((ctas * m + SLOTS - 1) / SLOTS) * chunks * 1.35 + 0.1 * m + 1.;
+        const double cost = (double)((ctas * m + SLOTS - 1) / SLOTS) * chunks * 1.35 + 0.05 * m + 1.;
         if (cost < best) {
             best = cost;
             sg.n = m;
