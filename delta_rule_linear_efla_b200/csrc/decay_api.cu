@@ -69,6 +69,7 @@ struct FwdPlan {
     Walks ws{};
     Segments sg{};
     Shares sh{};
+    float *S0 = nullptr;  // a copy of S0 where S_final replaces it: every stretch of a cut walk starts from it
     size_t bytes = 0;
     FwdPlan(int BH, int L, int dk, int dv, bool tc, void *base) {
         Arena ar{static_cast<char *>(base)};
@@ -77,6 +78,7 @@ struct FwdPlan {
         ws.w[0].b = dv;
         if (tc) sh = plan_shares(ws, BH, L, ar);
         else sg = plan_segments(ws, BH, L, ar);
+        if (tc ? sh.cut : sg.n > 1) S0 = ar.floats((size_t)BH * dk * dv);
         bytes = ar.used;
     }
 };
@@ -164,6 +166,11 @@ efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, co
     Walk &w = p.ws.w[0];
     w.x = q; w.y = k; w.z = v;
     w.s0 = S0;
+    if (S0 && S0 == S_final && p.S0) {
+        const cudaError_t e = cudaMemcpyAsync(p.S0, S0, state, cudaMemcpyDeviceToDevice, s);
+        if (e != cudaSuccess) return EFLA_ERR_CUDA;
+        w.s0 = p.S0;
+    }
     w.out = o;
     w.s_end = S_final;
     const Gate g{log_g, form == EFLA_DECAY_HEAD, dt == EFLA_BF16, H};

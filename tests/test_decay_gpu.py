@@ -123,6 +123,21 @@ def test_no_tokens_and_in_place_state(dtype, d):
     assert S is None
 
 
+@pytest.mark.parametrize("dtype,size", [(BF, (1, 1, 9000, 64, 128)), (BF, (2, 3, 2000, 128, 128)), (F32, (1, 1, 9000, 16, 24)),
+                                        (F32, (1, 2, 3000, 128, 100))])
+def test_in_place_state_of_sequences_that_are_cut(dtype, size):
+    """Every stretch of a cut sequence starts from S0, whichever of them ends first.  The state remembers up to 141
+    chunks: 141 * 2.4e-7 of truncation above the 3e-6 of one, below 4 * 2^-16; in fp32, 141 more roundings of u."""
+    q, k, v, l, S0 = make(*size, dtype, s0=True, seed=8)
+    l = l / 4096  # S0 counts up to the end
+    o, S = decay.decay_chunk_fwd(q, k, v, l, S0)
+    near(S, R.recurrence(q, k, v, l, S0)[1], 4 * STATE[dtype])
+    for _ in range(20):
+        carried = S0.clone()
+        o2, S2 = decay.decay_chunk_fwd(q, k, v, l, carried, S_final=carried)
+        assert S2 is carried and torch.equal(o, o2) and torch.equal(S, carried)
+
+
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
 def test_prompt_in_two_parts_then_decode(dtype, d):
     """A prompt in two calls, then tokens one at a time, is one call over all of it."""
