@@ -14,7 +14,7 @@
 // What bounds it (fp32, 8 x 32 x 256 tokens, d = 128: 319 us): shared memory's wavefronts (68 % of their
 // rate) and issue slots (59 %); a chunk of one column block takes 53,000 warp instructions, 29,000 of them FMAs.
 // Short sequences of few heads wait for their chain of chunks: cut into segments of two or more chunks,
-// 2 x 3 x 777 tokens take 46 us (76 with four or more, whose loads and joins waited for one another).
+// 2 x 3 x 777 tokens take 43 us (76 with four or more, whose loads and joins waited for one another).
 #include "decay_gate.cuh"
 #include "launchers.h"
 

@@ -24,11 +24,11 @@
 // running sums, off by at most 2^-10 where a chunk forgets everything at every token (sums of 18000) and 2^-15
 // with one such token: below the rounding of D o P.
 //
-// What bounds it (4 x 16 x 4096 tokens, d = 128: forward 95 us with its first pass, of which loads, stores and
-// hand-offs alone take 62 + 10; the three backward walks 315 us with theirs, of which 163): issue slots.  A
+// What bounds it (4 x 16 x 4096 tokens, d = 128: forward 94 us with its first pass, of which loads, stores and
+// hand-offs alone take 62 + 10; the three backward walks 311 us with theirs, of which 163): issue slots.  A
 // chunk takes about 1600 instructions a scheduler forwards and 2000 backwards, at half an instruction a
 // cycle; the tensor pipe is busy a quarter of the time.  At 1 x 16 x 65536 the forward's two passes move
-// 1.6 GB in 350 us.
+// 1.6 GB in 347 us.
 //
 // Warp roles (one CTA an SM, 24 warps):
 //   0-3   weight:  Yw's halves from Y's tile
