@@ -210,7 +210,10 @@ def decay_attention(q, k, v, log_g, S0=None, *, qk_norm: str | None = None, gate
     log_g of [H] is a constant of the model: one that requires a gradient is refused (expand it to [B,H,L]).
 
     qk_norm, gate, norm_weight, residual, scale, eps and act put the norms around it, as in
-    efla.efla_attention; with a gate the output is [B,L,H,dv]."""
+    efla.efla_attention; with a gate the output is [B,L,H,dv].
+
+    A backward pass can be captured into a CUDA graph; no eager autograd graph of the same leaves may be alive
+    then, since torch gathers a leaf's gradient on the stream of its first use, outside the capture."""
     from .norms import normed_attention
 
     if isinstance(log_g, torch.Tensor) and log_g.dim() == 1 and log_g.requires_grad:

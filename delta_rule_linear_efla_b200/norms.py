@@ -4,6 +4,7 @@ head_norm, before it: q or k out of a projection ([B,L,H,d], slices of a fused o
 normalised, in the attention's layout [B,H,L,d].  gated_norm, after it: the readout [B,H,L,d], each head
 normalised, gated, scaled and added to the residual, in the projections' layout [B,L,H,d].  Both are
 differentiable; *_fwd and *_bwd are the plain calls.  efla_attention and decay_attention take them along.
+Where a backward pass is captured into a CUDA graph, no eager autograd graph of the same leaves may be alive.
 """
 from __future__ import annotations
 
