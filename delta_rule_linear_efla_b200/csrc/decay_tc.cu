@@ -46,8 +46,7 @@
 
 #include "decay_gate.cuh"
 #include "launchers.h"
-#include "tc_ptx.cuh"
-#include "tmap.h"
+#include "tma_slabs.cuh"
 
 namespace efla {
 namespace decay {

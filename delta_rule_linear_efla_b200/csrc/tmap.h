@@ -38,22 +38,6 @@ inline bool make_3d(CUtensorMap *m, const void *ptr, uint64_t d0, uint64_t d1, u
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 16-bit tensor [d2][d1][64 slabs] as (64, d1, slabs, d2) with a (64, b1, slabs, 1) box: one load brings every
-// 64-element slab of b1 rows, slab after slab.
-inline bool make_slabs(CUtensorMap *m, const void *ptr, uint32_t slabs, uint64_t d1, uint64_t d2, uint32_t b1,
-                       CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t row = (cuuint64_t)slabs * 128;
-    const cuuint64_t dims[4] = {64, d1, slabs, d2};
-    const cuuint64_t strides[3] = {row, 128, row * d1};
-    const cuuint32_t box[4] = {64, b1, slabs, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return fn(m, dt, 4, const_cast<void *>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // 16-bit matrix [d1][d0] with a (b0, b1) box.
 inline bool make_2d(CUtensorMap *m, const void *ptr, uint64_t d0, uint64_t d1, uint32_t b0, uint32_t b1,
                     CUtensorMapDataType dt) {
