@@ -88,12 +88,17 @@ struct Bars {
     uint64_t full[NS], gready[2], y_free[2], pdone[2], d2done, o1done[2], o2done, o2read, drain[2], dfull[2], l_free;
     // one arrival from each of four warps
     uint64_t p_ready, s_ready;  // without output: an accumulator of the sum's parts is free again (pdone: it is full)
-    uint64_t gfree[2], o_free[2];  // the eight output warps (without output, gfree: the weights' sixteen)
+    // every warp that reads a batch's weights and that nothing else orders before it: the eight output warps and the
+    // weights' four (without output the weights' sixteen).  The mask's and the state's warps have read a chunk's
+    // before its p_ready and s_ready, which its output follows; the products that the output follows do not wait
+    // for its y_ready.
+    uint64_t gfree[2];
+    uint64_t o_free[2];                // the eight output warps
     uint64_t y_ready[2];               // the weights' four warps, sixteen without output
     uint64_t free_s[NS];               // one from each issuer
 };
 constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 1 + 2 + 2 + 2 + 3, BARS_FOUR = BARS_ONE + 2,
-              BARS_OUT = BARS_FOUR + 2 + 2, BARS_Y = BARS_OUT + 2;
+              BARS_GATE = BARS_FOUR + 2, BARS_OUT = BARS_GATE + 2, BARS_Y = BARS_OUT + 2;
 
 struct Slot {
     float qw[C];
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (tid == 0) {
         uint64_t *b = reinterpret_cast<uint64_t *>(&bars);
         for (int i = 0; i < BARS; ++i) 
-            tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS_FOUR ? 4 : i < BARS_OUT ? (OUT ? 8 : 16) : i < BARS_Y ? (OUT ? 4 : 16) : (OUT ? 2 : 1));
+            tc::mbar_init(b + i, i < BARS_ONE ? 1 : i < BARS_FOUR ? 4 : i < BARS_GATE ? (OUT ? 12 : 16) : i < BARS_OUT ? 8 : i < BARS_Y ? (OUT ? 4 : 16) : (OUT ? 2 : 1));
         tc::fence_mbar_init();
         abort_flag = 0;
         tc::tma_prefetch_desc(&maps.x[at.wi]);
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < PIECES; ++i) lo[i * T] = l[i];
             tc::fence_async_smem();
             warp_arrive(&bars.y_ready[n & 1], lane);
-            if (!OUT && lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
+            if (lane == 0 && n % GB == GB - 1) tc::mbar_arrive(&bars.gfree[n / GB & 1]);
         }
     } else if (!OUT && wg == 4) {
         // The stretch's contribution.  The tensor core truncates its fp32 sums, and a stretch is up to a hundred
