@@ -87,6 +87,7 @@ struct Bars {
     // one arrival (a commit, a thread, or a TMA load)
     uint64_t full[NS], gready[2], y_free[2], pdone[2], d2done, o1done[2], o2done, o2read, drain[2], dfull[2], l_free;
     // one arrival from each of four warps
+    uint64_t dread[2];          // backwards: an output group has read the dots' other factor
     uint64_t p_ready, s_ready;  // without output: an accumulator of the sum's parts is free again (pdone: it is full)
     // every warp that reads a batch's weights and that nothing else orders before it: the eight output warps and the
     // weights' four (without output the weights' sixteen).  The mask's and the state's warps have read a chunk's
@@ -97,7 +98,7 @@ struct Bars {
     uint64_t y_ready[2];               // the weights' four warps, sixteen without output
     uint64_t free_s[NS];               // one from each issuer
 };
-constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 1 + 2 + 2 + 2 + 3, BARS_FOUR = BARS_ONE + 2,
+constexpr int BARS = sizeof(Bars) / 8, BARS_ONE = NS + 2 + 2 + 2 + 1 + 2 + 2 + 2 + 3, BARS_FOUR = BARS_ONE + 4,
               BARS_GATE = BARS_FOUR + 2, BARS_OUT = BARS_GATE + 2, BARS_Y = BARS_OUT + 2;
 
 struct Slot {
@@ -792,13 +793,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int j = acc_row<B>(warp & 3, lane), h0 = wg == 3 ? 0 : 32;  // tokens h0 .. h0 + 31 of a chunk
         int loads = 0;  // of the dots' other factor: the group's half of a chunk's tile, by its first lane
         const int half = wg - 3;
+        const bool issuer = (warp & 3) == 0;
         uint8_t *dt = base + K::OFF_D + half * (K::ZB / 2);
 #pragma unroll 1
         for (int n = 0; n < cnt; ++n) {
             const int t0 = at.chunk(NC) * C + h0, cl = min(32, L - t0), bh = at.bh, wi = at.wi;
             const Walk &w = ws.w[wi];
             const bool split = BWD && w.dot != nullptr;
-            if (split) {  // every lane has read the last one
+            if (split) {  // once every warp has read the last one
+                if (issuer && loads > 0 && !wait(&bars.dread[half], loads - 1)) break;
                 if (gtid == 0) {
                     tc::mbar_expect_tx(&bars.dfull[half], K::ZB / 2);
                     tc::tma_load_4d(dt, &maps.d[wi], &bars.dfull[half], 0, t0, 0, bh);
@@ -846,12 +849,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint32_t u = *reinterpret_cast<const unsigned short *>(x + tc::sw128_off(i, c >> 3));
                     v[i] = B == 128 || j >= 0 ? v[i] * bf_lo(u) : 0.f;
                 }
-                tc::named_bar_sync(2 + half, 128);  // the tile is read
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.dread[half]);
                 const float s = column_sums(v, lane);
                 if (lane < cl) w.dot[((size_t)(warp & 3) * BH + bh) * L + t0 + lane] = s;
             }
         }
-        if (loads > 0) tc::mbar_wait(&bars.dfull[half], (loads - 1) & 1, budget / 8);  // nothing in flight at the end
+        if (issuer && loads > 0) tc::mbar_wait(&bars.dfull[half], (loads - 1) & 1, budget / 8);  // nothing in flight at the end
     }
     tc::tc_fence_before();
     __syncthreads();

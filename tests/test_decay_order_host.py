@@ -77,8 +77,8 @@ def steps(role, n, N, dots):
     if role == "state":
         return wait("d2done", n - 1) + gate() + [slot, ("write", "h", n), ("arrive", "s_ready", n)]
     assert role == "out"
-    load = [("write", "d", n), ("arrive", "dfull", n)] if dots else []
-    use = wait("dfull", n) + [("read", "d", n)] if dots else []  # one line: the group's warps meet after they have read
+    load = wait("dread", n - 1) + [("write", "d", n), ("arrive", "dfull", n)] if dots else []
+    use = wait("dfull", n) + [("read", "d", n), ("arrive", "dread", n)] if dots else []
     return (load + gate() + wait("o1done", n) + wait("o2read", n) + [("read", "o1_%d" % (n % no1), n), ("read", "o2", n), ("arrive", "o_free", n)] +
             [slot] + free + use)
 
@@ -171,3 +171,13 @@ def test_arrivals_are_counted():
     src, roles = code()
     count = re.search(r"i < BARS_GATE \? \(OUT \? (\d+) : 16\)", src)
     assert count and int(count.group(1)) == sum(WARPS[r] for r in ROLES if r in WARPS and "mbar_arrive(&bars.gfree" in roles[r])
+
+
+def test_no_role_waits_without_a_bound():
+    """Once the roles' loops run, a warp that has given up and left meets the others again at the kernel's end only: no
+    other barrier of the whole block or of a group, which waits for those that have left."""
+    _, roles = code()
+    for role, text in roles.items():
+        assert not re.search(r"named_bar_sync|__syncthreads|bar\.sync|barrier\.", text), role
+        for call in re.findall(r"tc::mbar_wait\(.*", text):  # what is in flight lands: bounded
+            assert "budget" in call, (role, call)
