@@ -135,20 +135,20 @@ __device__ __forceinline__ bool try_wait(uint32_t addr, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
+// By whole warps, whose lanes get one answer: a lane that gave up alone would leave the others of its warp behind, at
+// the next instruction that takes all of them.
 __device__ __noinline__ bool wait_longer(uint32_t addr, uint32_t parity, volatile int *abort_flag) {
     const long long t0 = clock64();
-    while (!try_wait(addr, parity)) {
-        if (*abort_flag) return false;
-        if (clock64() - t0 > WAIT_BUDGET) {
-            *abort_flag = 1;
-            return false;
-        }
+    while (!__all_sync(0xffffffffu, try_wait(addr, parity))) {
+        const bool late = clock64() - t0 > WAIT_BUDGET;
+        if (late) *abort_flag = 1;
+        if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
     }
     return true;
 }
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort_flag) {
     const uint32_t addr = tc::smem_u32(bar);
-    return try_wait(addr, parity) || wait_longer(addr, parity, abort_flag);
+    return __all_sync(0xffffffffu, try_wait(addr, parity)) || wait_longer(addr, parity, abort_flag);
 }
 
 // 16 lanes x 16 columns of tensor memory, a row of eight columns on four threads: v[4 k + 2 e + i] is row
@@ -350,8 +350,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0), lane_base = (uint32_t)(32 * (warp & 3)) << 16, sb = tc::smem_u32(base);
     const long long budget = WAIT_BUDGET;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_bar(bar, parity & 1, &abort_flag); };
-    // for the issuing warps: the same answer in every lane, so that descriptors stay in uniform registers
-    auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     auto wait_gate = [&](int n) { return n % GB != 0 || wait(&bars.gready[n / GB & 1], n / SLOTS); };
 
     // The state that enters a walk, or a place in it over the stretches [f0, f1) before it, into tensor memory:
@@ -429,12 +427,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         int st = 0, ph = 0;  // stage and its pass
         for (int n = 0; n < cnt; ++n) {
             const uint64_t o = (uint64_t)(st * (K::STAGE >> 4));
-            if (!wait_all(&bars.full[st], ph) || (OUT && !wait_all(&bars.s_ready, n))) break;
+            if (!wait(&bars.full[st], ph) || (OUT && !wait(&bars.s_ready, n))) break;
             tc::tc_fence_after();
             if (OUT) {
                 // O1^T = S^T X^T, before the state changes: its copy is then free when the new state is there
                 const int ob = n % K::NO1, m = n - K::NO1;  // read by the output of chunk m
-                if (m >= 0 && !wait_all(&bars.o_free[m & 1], m >> 1)) break;
+                if (m >= 0 && !wait(&bars.o_free[m & 1], m >> 1)) break;
                 tc::tc_fence_after();
                 const bool split = BWD && ws.w[at.wi].dot;
                 if (elect()) {
@@ -449,9 +447,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
             }
-            if (!wait_all(&bars.y_ready[n & 1], n >> 1)) break;
+            if (!wait(&bars.y_ready[n & 1], n >> 1)) break;
             const int part = n / FL;  // first pass: of the sum, in one of two accumulators
-            if (!OUT && n % FL == 0 && part >= 2 && !wait_all(part & 1 ? &bars.s_ready : &bars.p_ready, part / 2 - 1)) break;
+            if (!OUT && n % FL == 0 && part >= 2 && !wait(part & 1 ? &bars.s_ready : &bars.p_ready, part / 2 - 1)) break;
             const uint32_t acc = tmem + K::T_S + (OUT ? 0 : (part & 1) * A);
             tc::tc_fence_after();
             if (elect()) {  // S^T += Z^T Yw
@@ -502,12 +500,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ++ph;
             }
             if (n + 1 < cnt) {
-                if (!wait_all(&bars.full[st], ph)) break;
+                if (!wait(&bars.full[st], ph)) break;
                 tc::tc_fence_after();
                 issue_p(n + 1, st);
             }
             if (n < 0) continue;
-            if (!wait_all(&bars.p_ready, n) || (n > 0 && !wait_all(&bars.o_free[(n - 1) & 1], (n - 1) >> 1))) break;
+            if (!wait(&bars.p_ready, n) || (n > 0 && !wait(&bars.o_free[(n - 1) & 1], (n - 1) >> 1))) break;
             tc::tc_fence_after();
             if (elect()) {  // O2^T = Z^T (D o P)^T
                 const uint64_t z = dz + (uint64_t)(cur * (K::STAGE >> 4));

@@ -181,3 +181,14 @@ def test_no_role_waits_without_a_bound():
         assert not re.search(r"named_bar_sync|__syncthreads|bar\.sync|barrier\.", text), role
         for call in re.findall(r"tc::mbar_wait\(.*", text):  # what is in flight lands: bounded
             assert "budget" in call, (role, call)
+
+
+def test_a_warp_gives_up_as_one():
+    """The answer of a wait is the same in every lane: what follows takes whole warps."""
+    with open(SRC) as f:
+        src = f.read()
+    wait = src[src.index("bool wait_longer("):src.index("// 16 lanes x 16 columns")]
+    for call in re.findall(r".*try_wait\(addr.*", wait):
+        assert "__all_sync(0xffffffffu, try_wait(addr, parity))" in call, call
+    assert re.search(r"if \(__any_sync\(0xffffffffu, [^;]*\*abort_flag\)\) return false;", wait)
+    assert wait.count("return false") == 1
