@@ -362,8 +362,11 @@ cudaError_t launch_t(const Walks &ws, Gate g, int BH, int L, const Segments &sg,
     }
     auto *full = walk_simt_kernel<T, TO, true>;
     auto *part = walk_simt_kernel<T, TO, false>;
-    cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e == cudaSuccess && sg.n > 1) e = cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // The most that any head size takes: the limit belongs to the kernel, and another thread's call of a smaller head
+    // size must not lower it between here and the launch.
+    const int most = Lay(128).total;
+    cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess && sg.n > 1) e = cudaFuncSetAttribute(part, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     if (sg.n == 1) {
         full<<<dim3(blocks * BH), NT, smem, s>>>(ws, sg, g, BH, L);
