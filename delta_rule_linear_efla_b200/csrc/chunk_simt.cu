@@ -232,9 +232,11 @@ static cudaError_t launch_simt_t(const void *q, const void *k, const void *v, co
     const int NV = dv < SIMT_NV ? dv : SIMT_NV;
     const SimtSmem lay(dk, chunk, NV);
     dim3 grid(B * H, (dv + NV - 1) / NV);
+    // The most that any size takes: the limit belongs to the kernel, and another thread's call of smaller sizes
+    // must not lower it between here and the launch.
     cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<T, TO>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)lay.total);
+                                         (int)SimtSmem(128, 64, SIMT_NV).total);
     if (e != cudaSuccess) return e;
     chunk_simt_kernel<T, TO><<<grid, SIMT_THREADS, lay.total, s>>>(
         (const T *)q, (const T *)k, (const T *)v, (const T *)beta, (const T *)g, S0, (TO *)o, S_final,

@@ -25,7 +25,19 @@ def _decay(d, g):
     return call, o
 
 
-@pytest.mark.parametrize("make", [_decay])
+def _delta(d, g):
+    q, k, v = ((0.2 * torch.randn((1, 2, 130, d), generator=g)).cuda() for _ in range(3))
+    beta, o = torch.rand((1, 2, 130), generator=g).cuda(), torch.empty_like(v)
+    p, f = [t.data_ptr() for t in (q, k, v, beta)], efla.load_library().efla_chunk_fwd
+
+    def call(stream):
+        return f(*p, None, o.data_ptr(), None, 1, 2, 130, d, d, 64, efla.EFLA_F32, efla.EFLA_F32, None, 0, stream)
+
+    call.keep = (q, k, v, beta)
+    return call, o
+
+
+@pytest.mark.parametrize("make", [_decay, _delta])
 def test_host_threads_with_other_head_sizes(make):
     """Head sizes 128 and 16 in fp32 share their kernels, and need other amounts of shared memory."""
     g = torch.Generator().manual_seed(1)
