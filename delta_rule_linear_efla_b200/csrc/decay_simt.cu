@@ -384,13 +384,15 @@ cudaError_t launch_t(const Walks &ws, Gate g, int BH, int L, const Segments &sg,
 constexpr int DL_T = 512, DL_E = 8;  // tokens at once: 4096
 
 // One CTA per head, 4096 tokens at a time from the end: a block-wide suffix sum in fp64 (the differences q.dq - k.dk
-// of a long sequence cancel down to the pairs that straddle a token).
+// of a long sequence cancel down to the pairs that straddle a token).  At a token that forgets everything the sum is
+// zero by definition, and starts anew before it: the rounding of what is behind does not reach the documents in front.
 template <typename T>
 __global__ void __launch_bounds__(DL_T)
     dlog_kernel(const float *__restrict__ dotq, int nq, const float *__restrict__ dotk, int nk,
                 const float *__restrict__ dS, const float *__restrict__ S_end, const Gate g, T *__restrict__ dlog,
                 int BH, int L, int dk, int dv) {
     __shared__ double part[DL_T / 32];
+    __shared__ int part_cut[DL_T / 32];
     __shared__ double carry_s;
     const int bh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     cudaGridDependencySynchronize();
@@ -432,28 +434,49 @@ __global__ void __launch_bounds__(DL_T)
                 for (int e = 0; e < DL_E; ++e) x[e] += i < nq ? (double)v[e] : -(double)v[e];
             }
         }
+        // sums within the thread, from its end or from the last forgetting token on
+        unsigned forgets = 0;  // bit e: token t0 + e
 #pragma unroll
-        for (int e = DL_E - 2; e >= 0; --e) x[e] += x[e + 1];
-        double s = x[0];  // inclusive over the threads behind
+        for (int e = 0; e < DL_E; ++e)
+            if (t0 + e < L && gate_at(g, bh, L, t0 + e) == L_MIN) forgets |= 1u << e;
+#pragma unroll
+        for (int e = DL_E - 1; e >= 0; --e) x[e] = forgets >> e & 1 ? 0.0 : e + 1 < DL_E ? x[e] + x[e + 1] : x[e];
+        // over the warp's threads from this one on; cut: up to a forgetting token among them
+        double s = x[0];
+        int cut = forgets != 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double y = __shfl_down_sync(0xffffffffu, s, o);
-            if (lane + o < 32) s += y;
+            const int c = __shfl_down_sync(0xffffffffu, cut, o);
+            if (lane + o < 32 && !cut) {
+                s += y;
+                cut = c;
+            }
         }
-        if (lane == 0) part[warp] = s;
+        if (lane == 0) {
+            part[warp] = s;
+            part_cut[warp] = cut;
+        }
+        // what reaches this thread from behind: the rest of its warp, the warps behind, the tokens behind them
+        double behind = __shfl_down_sync(0xffffffffu, s, 1);
+        cut = __shfl_down_sync(0xffffffffu, cut, 1);
+        if (lane == 31) {
+            behind = 0.0;
+            cut = 0;
+        }
         __syncthreads();
-        double behind = carry + (s - x[0]);
-        for (int i = DL_T / 32 - 1; i > warp; --i) behind += part[i];
+        for (int i = warp + 1; i < DL_T / 32 && !cut; ++i) {
+            behind += part[i];
+            cut = part_cut[i];
+        }
+        if (!cut) behind += carry;
 #pragma unroll
         for (int e = 0; e < DL_E; ++e) {
             const int t = t0 + e;
-            if (t < L) {
-                // a token that forgets everything: d e^l / dl = 0
-                const bool forgets = gate_at(g, bh, L, t) == L_MIN;
-                dlog[row + t] = from_f32<T>(forgets ? 0.f : (float)(behind + x[e]));
-            }
+            if (forgets >> e == 0) x[e] += behind;
+            if (t < L) dlog[row + t] = from_f32<T>((float)x[e]);
         }
-        if (tid == 0) carry_s = behind + x[0];
+        if (tid == 0) carry_s = x[0];
         __syncthreads();
         carry = carry_s;
     }
