@@ -255,8 +255,11 @@ __global__ void __launch_bounds__(NT, 4)
 }
 
 // ------------------------------------------------------------------ gated norm
-// 1 / (1 + e^-x).  With bf16 gates the fast exponential and division, a few ulp off: far below the rounding of
-// anything that is made from it (and 0 below -87, where e^-x leaves the division's range).
+// 1 / (1 + e^-x).  Where everything made from it is bf16, the fast exponential and division: off by 2 + 1.17 |x| ulp
+// and 2 ulp (at most 1.3e-5 of the value, for gates near -87), far below bf16's rounding; and 0 below -87, where e^-x
+// leaves the division's range.  An fp32 weight's gradient is summed from those values too: the relative error is that
+// of its terms, and those of gates far below zero, whose error is large, count least.  Outputs in fp32 (a gate's
+// own type forwards, the gate's or o's backwards) take the accurate ones.
 template <bool ACCURATE>
 __device__ __forceinline__ float sigmoid_of(float x) {
     if constexpr (ACCURATE) return 1.f / (1.f + expf(-x));
@@ -309,7 +312,7 @@ __global__ void __launch_bounds__(NT, 4)
     gated_norm_bwd_kernel(const TO *__restrict__ o, const View gate, const Weight w, const T *__restrict__ dy,
                           TO *__restrict__ d_o, T *__restrict__ dgate, float *__restrict__ part, const Sizes n,
                           unsigned rows, bool silu, float scale, float eps) {
-    constexpr bool ACC = sizeof(T) == 4;
+    constexpr bool ACC = sizeof(T) == 4 || sizeof(TO) == 4;
     const Group<VEC, NV, G> g;
     constexpr unsigned RPC = NT / G;
     const float m = 1.f / n.d;
