@@ -207,7 +207,8 @@ class DecayFunction(torch.autograd.Function):
 def decay_attention(q, k, v, log_g, S0=None, *, qk_norm: str | None = None, gate=None, norm_weight=None, residual=None,
                     scale: float = 1.0, eps: float = 1e-6, act: str = "silu"):
     """Differentiable decay_chunk_fwd: (o, S_final), with gradients to q, k, v, log_g ([B,H,L]) and S0.  A
-    log_g of [H] is a constant of the model: one that requires a gradient is refused (expand it to [B,H,L]).
+    log_g of [H] is a constant of the model: one that requires a gradient is refused.  A learned one is given for every
+    token, log_g[:, None].expand(B, H, L).to(q.dtype).contiguous(), and gets its gradient through that.
 
     qk_norm, gate, norm_weight, residual, scale, eps and act put the norms around it, as in
     efla.efla_attention; with a gate the output is [B,L,H,dv].
@@ -217,6 +218,7 @@ def decay_attention(q, k, v, log_g, S0=None, *, qk_norm: str | None = None, gate
     from .norms import normed_attention
 
     if isinstance(log_g, torch.Tensor) and log_g.dim() == 1 and log_g.requires_grad:
-        raise ValueError("log_g of [H] has no gradient: expand it to [B,H,L]")
+        raise ValueError("log_g of [H] has no gradient: give one for every token, log_g[:, None].expand(B, H, L).to(q.dtype)"
+                         ".contiguous()")
     return normed_attention(lambda q, k: DecayFunction.apply(q, k, v, log_g, S0), q, k, qk_norm, gate, norm_weight,
                             residual, scale, eps, act)
