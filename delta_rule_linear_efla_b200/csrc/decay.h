@@ -18,7 +18,7 @@
 //   dl_t = sum_{u >= t} (q_u . dq_u - k_u . dk_u) + <dS_final, S_final>
 //
 // The last line: dl_t = e^{l_t} <dL/dS_t, S_{t-1}> = <dL/dS_t, S_t> - k_t . dk_t, and <dL/dS_t, S_t> =
-// q_t . dq_t + dl_{t+1}.
+// q_t . dq_t + dl_{t+1}.  The sum ends before the next token that forgets everything, whose dl is zero.
 #pragma once
 
 #include <cuda_runtime.h>

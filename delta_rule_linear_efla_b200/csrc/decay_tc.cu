@@ -24,11 +24,13 @@
 // running sums, off by at most 2^-10 where a chunk forgets everything at every token (sums of 18000) and 2^-15
 // with one such token: below the rounding of D o P.
 //
-// What bounds it (4 x 16 x 4096 tokens, d = 128: forward 94 us with its first pass, of which loads, stores and
-// hand-offs alone take 62 + 10; the three backward walks 311 us with theirs, of which 163): issue slots.  A
-// chunk takes about 1600 instructions a scheduler forwards and 2000 backwards, at half an instruction a
-// cycle; the tensor pipe is busy a quarter of the time.  At 1 x 16 x 65536 the forward's two passes move
-// 1.6 GB in 347 us.
+// What bounds it (4 x 16 x 4096 tokens, d = 128: forward 94 us with its first pass, 87 in a loop of that call alone;
+// the three backward walks 309 to 322 us with theirs): the latency of a chunk's chain of hand-offs (the state's copy,
+// its products, the state again), under which one CTA an SM has nothing else to run, and the bytes.  Loads and
+// hand-offs alone take 63 of the 87 us and 163 of 305; leaving out any one role's arithmetic changes the forward by
+// at most 6 %, the gradients by at most 12 %.  Issue slots are busy 42 to 52 % of the time, the tensor pipe 16 to 38 %.
+// At 1 x 16 x 65536 the forward's two passes move 1.6 GB in 345 us (296 before the power limit takes the clock from
+// 1965 to 1500 MHz).
 //
 // Warp roles (one CTA an SM, 24 warps):
 //   0-3   weight:  Yw's halves from Y's tile

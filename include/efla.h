@@ -410,7 +410,8 @@ efla_status efla_decay_chunk_fwd(const void *q, const void *k, const void *v, co
 /*
  * efla_decay_bwd -- its gradients, given dO = dL/do ([B,H,L,dv], dt) and dS_final =
  * dL/dS_final (fp32, or NULL for 0): dq, dkey [B,H,L,dk] and dval [B,H,L,dv] in dt, dlog_g
- * = dL/dl ([B,H,L], dt) or NULL, dS0 (fp32) or NULL.  A token with l = -inf has dlog_g = 0.
+ * = dL/dl ([B,H,L], dt) or NULL, dS0 (fp32) or NULL.  A token with l = -inf has dlog_g = 0, and
+ * nothing behind it adds to the dlog_g of those in front of it.
  * The per-head form is a constant of the model and has no gradient here: EFLA_ERR_OPTION
  * where dlog_g is given with it.  The outputs must not alias an input or one another.
  * workspace: efla_decay_bwd_workspace_size(...) bytes, 16-byte aligned.
