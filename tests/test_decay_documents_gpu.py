@@ -11,7 +11,7 @@ and the two halves of the states' copies add in a row of L tokens is at most 2^-
 import pytest
 import torch
 
-import decay_ref as R
+from decay_walked_ref import walked_gradients
 from delta_rule_linear_efla_b200 import decay, efla
 from test_decay_gpu import BF, F32, OUT, STATE, make, near
 
@@ -23,7 +23,7 @@ INF = float("inf")
 
 def check(x, dO, dS, got, level=1):
     """Every gradient; a log-decay of -inf has exactly none.  level: of the state's tolerance."""
-    ref = R.walked_gradients(*x, dO, dS)
+    ref = walked_gradients(*x, dO, dS)
     dtype = x[0].dtype
     for a, b in zip(got[:3], ref[:3]):
         near(a, b, OUT[dtype])
@@ -91,7 +91,7 @@ def test_gradients_past_32_bits():
     got = decay.decay_bwd(q, k, v, l, dO)
     n, m = 5000, 1000
     tail = [t[:, -1:, -n:].contiguous() for t in (q, k, v, l)]
-    ref = R.walked_gradients(*tail, None, dO[:, -1:, -n:].contiguous(), None)
+    ref = walked_gradients(*tail, None, dO[:, -1:, -n:].contiguous(), None)
     for a, b in zip(got[:3], ref[:3]):
         near(a[:, -1:, -m:], b[:, :, -m:], OUT[BF])
     near(got[3][:, -1:, -m:], ref[3][:, :, -m:], DL[BF])

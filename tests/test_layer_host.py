@@ -142,18 +142,3 @@ def test_reference_gradients_against_differences():
         up, down = list(x), list(x)
         up[i], down[i] = x[i] + 1e-5 * d, x[i] - 1e-5 * d
         assert abs((f(up) - f(down)) / 2e-5 - float((grads[i] * d).sum())) <= 1e-7
-
-
-def test_walked_reference_gradients():
-    """The reference for long rows is autograd's through the recurrence, over several documents too."""
-    g = torch.Generator().manual_seed(2)
-
-    def n(*s):
-        return torch.randn(s, generator=g, dtype=torch.float64)
-
-    x = [n(1, 2, 9, 3), n(1, 2, 9, 3), n(1, 2, 9, 4), -n(1, 2, 9).abs(), n(1, 2, 3, 4)]
-    x[3][0, 0, 4] = x[3][0, 1, 2] = x[3][0, 1, 7] = -300.0
-    dO, dS = n(1, 2, 9, 4), n(1, 2, 3, 4)
-    for args in ((x[4], dO, dS), (None, dO, None)):
-        for a, b in zip(R.walked_gradients(*x[:4], *args), R.gradients(*x[:4], *args)):
-            assert (a - b).abs().max() <= 1e-12
